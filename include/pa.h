@@ -21,7 +21,7 @@
  *
  * Conventions shared by every call
  *   - Memory: every pointer argument named *_cache, q, k, v, out, slot_mapping, block_tables,
- *     context_lens, query_start_loc and workspace is a DEVICE pointer on the current device.
+ *     context_lens, query_start_loc, key_weights and workspace is a DEVICE pointer on the current device.
  *     `cache` descriptors are HOST pointers.  The caller allocates and owns all of it; the
  *     library never allocates or frees device memory.
  *   - Execution: calls are asynchronous on `stream` (0 = legacy default stream) and ordered by
@@ -39,6 +39,13 @@
  *   block pool:  k_cache, v_cache = [num_blocks][num_kv_heads][block_size][head_dim], elements
  *                bf16, or OCP E4M3 bytes holding x / k_scale (resp. v_scale) with fp32 per-tensor
  *                scales.  One (block, kv head) tile of block_size x head_dim is contiguous.
+ *                PA_MXFP4 pools (microscaled 4-bit floating point): 32 neighbouring dims of a row
+ *                share a scale byte e (E8M0: 2^(e - 127), 255 = NaN), and a dim is a 4-bit E2M1
+ *                code c (0 .5 1 1.5 2 3 4 6, bit 3 the sign): value = code * 2^(e - 127).  One
+ *                (block, kv head) tile is 17 * head_dim / 2 contiguous bytes: 16 rows of
+ *                head_dim / 2 bytes of codes, then 16 rows of head_dim / 32 scale bytes.  With
+ *                nb = head_dim / 32, 16-bit word g * nb + b of a row (little endian) holds dims
+ *                32 b + 4 g .. 32 b + 4 g + 3, the lowest dim in its lowest four bits.
  *   slot:        physical_block * block_size + offset; a negative slot means "skip".
  *   new k, v:    [num_tokens][num_kv_heads][head_dim] bf16.
  *   q, out:      [num_q_tokens][num_q_heads][head_dim]; q bf16, out fp32 or bf16.
@@ -72,17 +79,17 @@ typedef enum {
   PA_ERR_CUDA = 5          /* a CUDA runtime call failed; see pa_last_error_string */
 } pa_status;
 
-typedef enum { PA_BF16 = 0, PA_FP8_E4M3 = 1, PA_FP32 = 2 } pa_dtype;
+typedef enum { PA_BF16 = 0, PA_FP8_E4M3 = 1, PA_FP32 = 2, PA_MXFP4 = 3 } pa_dtype;
 
 /* Geometry of one pool (both k_cache and v_cache).  Supported: block_size 16; head_dim 64 or
- * 128 for bf16, 128 for PA_FP8_E4M3; num_blocks * num_kv_heads * block_size (the pool's rows)
+ * 128 for bf16 and PA_MXFP4, 128 for PA_FP8_E4M3; num_blocks * num_kv_heads * block_size (the pool's rows)
  * at most 2^31 - 1.  k_scale / v_scale are used only for PA_FP8_E4M3. */
 typedef struct {
   int32_t num_blocks;
   int32_t block_size;
   int32_t num_kv_heads;
   int32_t head_dim;
-  int32_t cache_dtype; /* pa_dtype: PA_BF16 or PA_FP8_E4M3 */
+  int32_t cache_dtype; /* pa_dtype: PA_BF16, PA_FP8_E4M3 or PA_MXFP4 */
   float k_scale;
   float v_scale;
 } pa_cache_desc;
@@ -97,6 +104,7 @@ typedef struct {
 #define PA_DEVERR_SLOT 0x2u        /* slot >= num_blocks * block_size */
 #define PA_DEVERR_LENGTHS 0x4u     /* n_s < 0, n_s > context_len, or a host hint exceeded */
 #define PA_DEVERR_TIMEOUT 0x8u     /* bounded wait expired */
+#define PA_DEVERR_WEIGHT_ROW 0x10u /* weight row >= num_weight_rows */
 
 /* Scatter new keys/values into the pool.
  *   k, v          [num_tokens][num_kv_heads][head_dim] bf16 (device).
@@ -105,11 +113,24 @@ typedef struct {
  *   workspace     >= PA_WORKSPACE_HEADER_BYTES bytes (device); receives PA_DEVERR_SLOT.
  * bf16 pools receive the bits unchanged.  E4M3 pools receive, per element, the E4M3 encoding
  * (round to nearest even, saturating to +-448) of the fp32 quotient x / scale rounded to
- * nearest.  num_tokens == 0 is a no-op.  A slot written twice in one call ends up holding one
+ * nearest.  MXFP4 pools receive, per block of 32 dims, the scale 2^e with e = floor(log2(amax)) -
+ * 2 (at least -127; amax the block's largest magnitude) and, per element, x / 2^e rounded to the
+ * nearest E2M1 value (ties to the even code, saturating at +-6); a block with a NaN receives the
+ * NaN scale and zero codes.  num_tokens == 0 is a no-op.  A slot written twice in one call ends up holding one
  * of the writes. */
 pa_status pa_cache_append(const void* k, const void* v, const int64_t* slot_mapping,
                           int32_t num_tokens, void* k_cache, void* v_cache,
                           const pa_cache_desc* cache, void* workspace, cudaStream_t stream);
+
+/* Read slots back: the values that the pool holds for slot_mapping[t], rounded once to out_dtype
+ * (exact for bf16 and MXFP4 pools, and in fp32 for E4M3 up to the product with its scale).
+ *   slot_mapping  [num_tokens] int64 (device).  The rows of a negative slot are zeros, and so are
+ *                 those of a slot past the pool, which also sets PA_DEVERR_SLOT.
+ *   k, v          [num_tokens][num_kv_heads][head_dim], out_dtype PA_FP32 or PA_BF16 (device).
+ *   workspace     >= PA_WORKSPACE_HEADER_BYTES bytes (device). */
+pa_status pa_cache_read(const int64_t* slot_mapping, int32_t num_tokens, const void* k_cache,
+                        const void* v_cache, const pa_cache_desc* cache, void* k, void* v,
+                        int32_t out_dtype, void* workspace, cudaStream_t stream);
 
 /* Copy whole blocks inside the pool: for each pair i, block block_pairs[2i] (source) is copied
  * to block block_pairs[2i+1] (destination), all kv heads, K and V, bit for bit.
@@ -150,6 +171,8 @@ size_t pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_tokens, int32
  * 128 or 64 or an E4M3 pool of head_dim 128 and query runs of more than 16 tokens or more than
  * 16 (token x q head) rows, the tensor-core prefill tiles on the part of the SMs the plan gives
  * them, the split-KV kernel on the rest, and the merge of split sequences.
+ * MXFP4 pools have their own split-KV kernel, which takes runs of any length in tiles of up to 32
+ * rows.
  * Work enqueued on `stream` after the call sees all of it complete.  The call records no event
  * and creates no stream, so it can be captured into a CUDA graph like any kernel launch. */
 pa_status pa_attention(const void* q, int32_t num_q_tokens, const void* k_cache,
@@ -160,6 +183,77 @@ pa_status pa_attention(const void* q, int32_t num_q_tokens, const void* k_cache,
                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
                        void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes,
                        cudaStream_t stream);
+
+/* Workspace bytes pa_attention_key_weights needs for a step of this shape (host-only). */
+size_t pa_attention_key_weights_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
+                                               int32_t num_q_heads, int32_t num_kv_heads,
+                                               int32_t head_dim, int32_t block_size,
+                                               int32_t max_context_len, int32_t max_query_len);
+
+/* pa_attention that also accumulates how much attention every cached key received, the measure by
+ * which pa_evict_keys chooses.  Of a sequence s with query tokens, for every kv head h and key j
+ * of its context_lens[s] keys:
+ *   W[row][h][j] <- decay * W[row][h][j] + sum of the softmax weights of key j over the step's
+ *                   query tokens that attend it and the q heads of h's group.
+ *   key_weights   [num_weight_rows][num_kv_heads][max_keys] fp32 (device), updated in place;
+ *                 max_keys >= max_context_len.  A caller zeroes a row when a sequence starts to
+ *                 use it: positions appended later then begin at 0.
+ *   weight_rows   [num_seqs] int32 (device): the row of each sequence, or NULL for row s.  The
+ *                 weights of a sequence with a negative row, or without query tokens, are left as
+ *                 they are; a row >= num_weight_rows sets PA_DEVERR_WEIGHT_ROW and is skipped.
+ *                 Two sequences must not share a row: it ends up with one of the results.
+ *   decay         >= 0; 1 sums over all steps.
+ * The other arguments, the output and the errors are pa_attention's (a sequence that it skips
+ * accumulates nothing; nor does a key in a block outside the pool).  The sums are fp32 and their
+ * order is fixed: the same call gives the same bits. */
+pa_status pa_attention_key_weights(
+    const void* q, int32_t num_q_tokens, const void* k_cache, const void* v_cache,
+    const pa_cache_desc* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
+    int32_t max_context_len, int32_t max_query_len, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, float scale, void* out, int32_t out_dtype, float* key_weights,
+    const int32_t* weight_rows, int32_t num_weight_rows, int32_t max_keys, float decay,
+    void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes pa_evict_keys needs (host-only). */
+size_t pa_evict_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t max_context_len,
+                               int32_t max_keep_len);
+
+/* Drop the keys that received the least attention.  Of a sequence's L = context_lens[s] keys, k =
+ * min(keep_lens[s], L) stay, chosen per kv head: the last min(recent, k) and, of the others, those
+ * of the largest key_weights (ties: the lowest position; NaN counts as -infinity).  Kept keys
+ * and values move, in their order, to positions 0 .. k - 1 of dst_tables; a later step attends
+ * them with context_lens[s] = new_lens[s] (and its new tokens after them).
+ *   block_tables  [num_seqs][max_blocks_per_seq] int32 (device): where the keys are.
+ *   dst_tables    the same shape: where they go, or NULL for block_tables (in place).  Entry i may
+ *                 be block_tables' entry i, or a block that no sequence of the call reads; no
+ *                 block may be a destination of two sequences, and none that another sequence
+ *                 reads may be a destination (pa_bm_evict gives such tables); otherwise the
+ *                 blocks' contents are undefined.
+ *   keep_lens     [num_seqs] int32 (device), >= 0.
+ *   max_context_len, max_keep_len   host upper bounds of context_lens and of k.
+ *   key_weights, weight_rows, num_weight_rows, max_keys   as in pa_attention_key_weights.  The
+ *                 weights of the kept keys move with them to row dst_weight_rows[s] (NULL: the
+ *                 same row), whose positions k .. L - 1 become 0; later positions stay as they
+ *                 are.  A destination row must not be another sequence's row of either kind.
+ *   kept          [num_seqs][num_kv_heads][max_keep_len] int32 (device): the old positions of the
+ *                 kept keys, ascending, then -1.
+ *   new_lens      [num_seqs] int32 (device): k.  It may not overlap context_lens, keep_lens or the
+ *                 row tables.
+ *   workspace     >= pa_evict_workspace_size(...) bytes (device).
+ * A sequence with a negative length, more keys than max_context_len or its table hold, a k above
+ * max_keep_len (PA_DEVERR_LENGTHS), or a row past key_weights (PA_DEVERR_WEIGHT_ROW) or negative
+ * (no error) is left as it is: its new_lens is its context length and its kept are -1.  A block
+ * outside the pool sets PA_DEVERR_BLOCK_ID and its keys do not move. */
+pa_status pa_evict_keys(void* k_cache, void* v_cache, const pa_cache_desc* cache,
+                        const int32_t* block_tables, const int32_t* dst_tables,
+                        int32_t max_blocks_per_seq, const int32_t* context_lens,
+                        const int32_t* keep_lens, int32_t num_seqs, int32_t max_context_len,
+                        int32_t max_keep_len, int32_t recent, float* key_weights,
+                        const int32_t* weight_rows, const int32_t* dst_weight_rows,
+                        int32_t num_weight_rows, int32_t max_keys, int32_t* kept,
+                        int32_t* new_lens, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream);
 
 /* Scratch bytes built into the library for pa_attention_noalloc (32 MiB per device). */
 #define PA_NOALLOC_SCRATCH_BYTES (32u * 1024u * 1024u)

@@ -78,6 +78,19 @@ int32_t pa_bm_fork(pa_block_manager* bm, int64_t parent, int64_t child);
  * free list, or to the evictable cache if it carries a hash).  Returns 0 or PA_BM_BAD_ARG. */
 int32_t pa_bm_free(pa_block_manager* bm, int64_t seq);
 
+/* Reduce seq to its first `keep` token positions before pa_evict_keys fills them with the kept
+ * keys.  The sequence's new table has ceil(keep / block_size) blocks: blocks that other
+ * sequences share are replaced by fresh ones, blocks that it holds alone stay (and leave the
+ * prefix cache, as their contents change); its other blocks are released.  The new table goes
+ * to table_out, padded with -1 to cap entries: with the table from before the call as
+ * block_tables it is pa_evict_keys' dst_tables.  Released blocks may be handed out by the next
+ * call, so pa_evict_keys must be launched before, on the same stream as, the kernels that write
+ * them.  Tokens appended later carry no hash.
+ * Returns the number of blocks, PA_BM_NO_SPACE, or PA_BM_BAD_ARG (unknown sequence, keep < 0 or
+ * above its tokens, cap too small). */
+int32_t pa_bm_evict(pa_block_manager* bm, int64_t seq, int64_t keep, int32_t* table_out,
+                    int32_t cap);
+
 /* Block table of seq into table_out[0..cap); returns the number of blocks (may exceed cap, in
  * which case only cap entries are written) or PA_BM_BAD_ARG. */
 int32_t pa_bm_block_table(const pa_block_manager* bm, int64_t seq, int32_t* table_out,

@@ -10,6 +10,14 @@ raise, there is no CPU fallback.
     pa.cache_append(k, v, slot_mapping, k_cache, v_cache, ws)
     out = pa.attention(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, ws,
                        scale=..., max_context_len=..., max_query_len=...)
+
+Smaller caches: pools of 4-bit floating point (``new_mxfp4_cache``, taken by every call), and
+eviction of the keys that received the least attention:
+
+    out = pa.attention_key_weights(q, k_cache, v_cache, block_tables, context_lens,
+                                   query_start_loc, key_weights, ws, scale=..., ...)
+    kept, context_lens = pa.evict_keys(k_cache, v_cache, block_tables, context_lens, keep_lens,
+                                       key_weights, ws, recent=..., ...)
 """
 
 from __future__ import annotations
@@ -20,10 +28,12 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import (PA_BF16, PA_FP8_E4M3, PA_FP32, PA_WORKSPACE_HEADER_BYTES,  # noqa: F401
-                   PagedAttnError)
+from ._lib import (PA_BF16, PA_FP8_E4M3, PA_FP32, PA_MXFP4,  # noqa: F401
+                   PA_WORKSPACE_HEADER_BYTES, PagedAttnError)
 
-__all__ = ["cache_append", "attention", "attention_workspace_size", "new_workspace",
+__all__ = ["cache_append", "cache_read", "new_mxfp4_cache", "attention",
+           "attention_key_weights", "attention_key_weights_workspace_size", "evict_keys",
+           "evict_workspace_size", "attention_workspace_size", "new_workspace",
            "check_error", "library", "version", "PagedAttnError", "set_kernel_timing_events",
            "set_prefill_timing_events", "set_kernel_span_buffer"]
 
@@ -61,7 +71,35 @@ def _need(t: torch.Tensor, name: str, dtypes, ndim: int):
 _FP8_DTYPES = (torch.uint8, torch.float8_e4m3fn)
 
 
+def new_mxfp4_cache(num_blocks: int, num_kv_heads: int, head_dim: int, device="cuda"
+                    ) -> torch.Tensor:
+    """A zeroed MXFP4 pool for the keys or the values: uint8 [num_blocks, num_kv_heads, 17 *
+    head_dim / 2], one tile of 16 rows of codes and their scale bytes per block and kv head."""
+    if head_dim not in (64, 128):
+        raise ValueError("MXFP4 pools are built for head_dim 64 and 128")
+    return torch.zeros((num_blocks, num_kv_heads, head_dim * 17 // 2), dtype=torch.uint8,
+                       device=device)
+
+
+def _need_caches(k_cache: torch.Tensor, v_cache: torch.Tensor) -> None:
+    """k_cache / v_cache: [NB, Hkv, 16, D] bf16 or E4M3, or [NB, Hkv, 17 D / 2] uint8 (MXFP4)."""
+    mx = isinstance(k_cache, torch.Tensor) and k_cache.dim() == 3
+    _need(k_cache, "k_cache", (torch.uint8,) if mx else (torch.bfloat16,) + _FP8_DTYPES,
+          3 if mx else 4)
+    _need(v_cache, "v_cache", (k_cache.dtype,), k_cache.dim())
+
+
+def _same_shape(k_cache: torch.Tensor, v_cache: torch.Tensor) -> None:
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+
+
 def cache_desc(k_cache: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0):
+    if k_cache.dim() == 3:
+        nb, hkv, tile = k_cache.shape
+        if tile % 17:
+            raise ValueError("an MXFP4 pool has tiles of 17 * head_dim / 2 bytes")
+        return _lib.CacheDesc(nb, 16, hkv, tile * 2 // 17, PA_MXFP4, 1.0, 1.0)
     nb, hkv, bs, d = k_cache.shape
     dt = PA_FP8_E4M3 if k_cache.dtype in _FP8_DTYPES else PA_BF16
     return _lib.CacheDesc(nb, bs, hkv, d, dt, float(k_scale), float(v_scale))
@@ -82,14 +120,12 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
     _need(k, "k", (torch.bfloat16,), 3)
     _need(v, "v", (torch.bfloat16,), 3)
     _need(slot_mapping, "slot_mapping", (torch.int64,), 1)
-    _need(k_cache, "k_cache", (torch.bfloat16,) + _FP8_DTYPES, 4)
-    _need(v_cache, "v_cache", (k_cache.dtype,), 4)
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache shapes differ")
-    if k.shape != v.shape or k.shape[0] != slot_mapping.shape[0] or \
-            k.shape[1:] != (k_cache.shape[1], k_cache.shape[3]):
-        raise ValueError("k/v/slot_mapping shapes do not match the cache")
+    _need_caches(k_cache, v_cache)
+    _same_shape(k_cache, v_cache)
     desc = cache_desc(k_cache, k_scale, v_scale)
+    if k.shape != v.shape or k.shape[0] != slot_mapping.shape[0] or \
+            k.shape[1:] != (desc.num_kv_heads, desc.head_dim):
+        raise ValueError("k/v/slot_mapping shapes do not match the cache")
     L = _lib.load()
     _lib.check(L.pa_cache_append(_ptr(k), _ptr(v), _ptr(slot_mapping), k.shape[0],
                                  _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc),
@@ -112,8 +148,18 @@ def attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
               v_scale: float = 1.0, stream=None) -> torch.Tensor:
     """Ragged paged attention: q [T, Hq, D] bf16 -> out [T, Hq, D] (fp32 or bf16)."""
     _need(q, "q", (torch.bfloat16,), 3)
-    _need(k_cache, "k_cache", (torch.bfloat16,) + _FP8_DTYPES, 4)
-    _need(v_cache, "v_cache", (k_cache.dtype,), 4)
+    out, args = _step_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                           workspace, scale, max_context_len, max_query_len, out, out_dtype,
+                           k_scale, v_scale)
+    _lib.check(_lib.load().pa_attention(*args, _ptr(workspace), workspace.numel(),
+                                        _stream(stream)))
+    return out
+
+
+def _step_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, workspace, scale,
+               max_context_len, max_query_len, out, out_dtype, k_scale, v_scale):
+    """Checks one step's tensors; returns its output and the C arguments up to out_dtype."""
+    _need_caches(k_cache, v_cache)
     _need(block_tables, "block_tables", (torch.int32,), 2)
     _need(context_lens, "context_lens", (torch.int32,), 1)
     _need(query_start_loc, "query_start_loc", (torch.int32,), 1)
@@ -132,13 +178,153 @@ def attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
             raise ValueError("out has the wrong shape")
     odt = PA_FP32 if out.dtype == torch.float32 else PA_BF16
     desc = cache_desc(k_cache, k_scale, v_scale)
-    L = _lib.load()
-    _lib.check(L.pa_attention(
+    return out, (
         _ptr(q), T, _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc), _ptr(block_tables),
         block_tables.shape[1], _ptr(context_lens), _ptr(query_start_loc), S,
-        int(max_context_len), int(max_query_len), Hq, Hkv, D, float(scale), _ptr(out), odt,
-        _ptr(workspace), workspace.numel(), _stream(stream)))
+        int(max_context_len), int(max_query_len), Hq, Hkv, D, float(scale), _ptr(out), odt)
+
+
+def _on(stream, *tensors):
+    """Checks that the tensors (None: absent) share one device and returns a context in which the
+    call's allocations and its launch are on that device and on `stream` (None: the device's
+    current stream)."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {t.device} and {dev}")
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream of {stream.device} for tensors on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _need_weights(key_weights, num_kv_heads, num_seqs, **rows):
+    _need(key_weights, "key_weights", (torch.float32,), 3)
+    if key_weights.shape[1] != num_kv_heads:
+        raise ValueError("key_weights must be [rows, num_kv_heads, max_keys]")
+    for name, r in rows.items():
+        if r is not None:
+            _need(r, name, (torch.int32,), 1)
+            if r.shape[0] != num_seqs:
+                raise ValueError(f"{name} must have num_seqs entries")
+
+
+def attention_key_weights_workspace_size(num_seqs: int, num_q_tokens: int, num_q_heads: int,
+                                         num_kv_heads: int, head_dim: int, max_context_len: int,
+                                         max_query_len: int, block_size: int = 16) -> int:
+    return int(_lib.load().pa_attention_key_weights_workspace_size(
+        num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+        max_context_len, max_query_len))
+
+
+def attention_key_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          block_tables: torch.Tensor, context_lens: torch.Tensor,
+                          query_start_loc: torch.Tensor, key_weights: torch.Tensor,
+                          workspace: torch.Tensor, *, scale: float, max_context_len: int,
+                          max_query_len: int, weight_rows: Optional[torch.Tensor] = None,
+                          decay: float = 1.0, out: Optional[torch.Tensor] = None,
+                          out_dtype: torch.dtype = torch.float32, k_scale: float = 1.0,
+                          v_scale: float = 1.0, stream=None) -> torch.Tensor:
+    """`attention`, and key_weights [rows, Hkv, max_keys] (fp32) is updated in place: decayed,
+    plus the softmax weights each cached key received from the step's queries and the q heads of
+    its group.  weight_rows [num_seqs] (int32): the row of each sequence (None: row s)."""
+    _need(q, "q", (torch.bfloat16,), 3)
+    _need_caches(k_cache, v_cache)
+    _same_shape(k_cache, v_cache)
+    _need(context_lens, "context_lens", (torch.int32,), 1)
+    _need_weights(key_weights, k_cache.shape[1], context_lens.shape[0], weight_rows=weight_rows)
+    with _on(stream, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, key_weights,
+             workspace, weight_rows, out):
+        out, args = _step_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                               workspace, scale, max_context_len, max_query_len, out, out_dtype,
+                               k_scale, v_scale)
+        _lib.check(_lib.load().pa_attention_key_weights(
+            *args, _ptr(key_weights), _ptr(weight_rows), key_weights.shape[0],
+            key_weights.shape[2], float(decay), _ptr(workspace), workspace.numel(),
+            _stream(stream)))
     return out
+
+
+def evict_workspace_size(num_seqs: int, num_kv_heads: int, max_context_len: int,
+                         max_keep_len: int) -> int:
+    return int(_lib.load().pa_evict_workspace_size(num_seqs, num_kv_heads, max_context_len,
+                                                   max_keep_len))
+
+
+def evict_keys(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+               context_lens: torch.Tensor, keep_lens: torch.Tensor, key_weights: torch.Tensor,
+               workspace: torch.Tensor, *, max_context_len: int, max_keep_len: int, recent: int,
+               dst_tables: Optional[torch.Tensor] = None,
+               weight_rows: Optional[torch.Tensor] = None,
+               dst_weight_rows: Optional[torch.Tensor] = None,
+               kept: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+               stream=None):
+    """Keep keep_lens[s] keys of each sequence, per kv head: the last `recent` and those of the
+    largest key_weights; they move to the front of dst_tables' blocks (None: in place), their
+    weights with them.  Returns (kept [S, Hkv, max_keep_len] old positions, -1 past the kept ones;
+    new_lens [S])."""
+    _need_caches(k_cache, v_cache)
+    _same_shape(k_cache, v_cache)
+    _need(block_tables, "block_tables", (torch.int32,), 2)
+    _need(context_lens, "context_lens", (torch.int32,), 1)
+    _need(keep_lens, "keep_lens", (torch.int32,), 1)
+    _need(workspace, "workspace", (torch.uint8,), 1)
+    S, H = context_lens.shape[0], k_cache.shape[1]
+    _need_weights(key_weights, H, S, weight_rows=weight_rows, dst_weight_rows=dst_weight_rows)
+    if block_tables.shape[0] != S or keep_lens.shape[0] != S:
+        raise ValueError("block_tables and keep_lens must have num_seqs rows")
+    if dst_tables is not None:
+        _need(dst_tables, "dst_tables", (torch.int32,), 2)
+        if dst_tables.shape != block_tables.shape:
+            raise ValueError("dst_tables must have block_tables' shape")
+    if max_keep_len < 0:
+        raise ValueError("max_keep_len must not be negative")
+    with _on(stream, k_cache, v_cache, block_tables, context_lens, keep_lens, key_weights,
+             workspace, dst_tables, weight_rows, dst_weight_rows, kept, new_lens):
+        if kept is None:
+            kept = torch.empty((S, H, max_keep_len), dtype=torch.int32, device=k_cache.device)
+        else:
+            _need(kept, "kept", (torch.int32,), 3)
+            if tuple(kept.shape) != (S, H, max_keep_len):
+                raise ValueError("kept has the wrong shape")
+        if new_lens is None:
+            new_lens = torch.empty((S,), dtype=torch.int32, device=k_cache.device)
+        else:
+            _need(new_lens, "new_lens", (torch.int32,), 1)
+            if new_lens.shape[0] != S:
+                raise ValueError("new_lens has the wrong shape")
+        desc = cache_desc(k_cache)
+        _lib.check(_lib.load().pa_evict_keys(
+            _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc), _ptr(block_tables),
+            _ptr(dst_tables), block_tables.shape[1], _ptr(context_lens), _ptr(keep_lens), S,
+            int(max_context_len), int(max_keep_len), int(recent), _ptr(key_weights),
+            _ptr(weight_rows), _ptr(dst_weight_rows), key_weights.shape[0], key_weights.shape[2],
+            _ptr(kept), _ptr(new_lens), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return kept, new_lens
+
+
+def cache_read(slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+               workspace: torch.Tensor, *, out_dtype: torch.dtype = torch.bfloat16,
+               k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """The keys and values that the pools hold in slot_mapping [T] (int64): two tensors
+    [T, Hkv, D] (bf16 or fp32); zeros for negative slots."""
+    _need(slot_mapping, "slot_mapping", (torch.int64,), 1)
+    _need_caches(k_cache, v_cache)
+    _same_shape(k_cache, v_cache)
+    _need(workspace, "workspace", (torch.uint8,), 1)
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    desc = cache_desc(k_cache, k_scale, v_scale)
+    with _on(stream, slot_mapping, k_cache, v_cache, workspace):
+        k = torch.empty((slot_mapping.shape[0], desc.num_kv_heads, desc.head_dim),
+                        dtype=out_dtype, device=k_cache.device)
+        v = torch.empty_like(k)
+        _lib.check(_lib.load().pa_cache_read(
+            _ptr(slot_mapping), slot_mapping.shape[0], _ptr(k_cache), _ptr(v_cache),
+            ctypes.byref(desc), _ptr(k), _ptr(v),
+            PA_FP32 if out_dtype == torch.float32 else PA_BF16, _ptr(workspace), _stream(stream)))
+    return k, v
 
 
 def check_error(workspace: torch.Tensor, stream=None, raise_on_error: bool = True) -> int:

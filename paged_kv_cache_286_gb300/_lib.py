@@ -10,10 +10,11 @@ LIB_PATH = os.path.join(PKG, "libpagedattn.so")
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_OUT_OF_RANGE, PA_ERR_TIMEOUT, \
     PA_ERR_CUDA = range(6)
-PA_BF16, PA_FP8_E4M3, PA_FP32 = 0, 1, 2
+PA_BF16, PA_FP8_E4M3, PA_FP32, PA_MXFP4 = 0, 1, 2, 3
 PA_WORKSPACE_HEADER_BYTES = 256
 PA_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
-PA_DEVERR_BLOCK_ID, PA_DEVERR_SLOT, PA_DEVERR_LENGTHS, PA_DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+PA_DEVERR_BLOCK_ID, PA_DEVERR_SLOT, PA_DEVERR_LENGTHS, PA_DEVERR_TIMEOUT, \
+    PA_DEVERR_WEIGHT_ROW = 0x1, 0x2, 0x4, 0x8, 0x10
 
 STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED",
                 3: "PA_ERR_OUT_OF_RANGE", 4: "PA_ERR_TIMEOUT", 5: "PA_ERR_CUDA"}
@@ -22,11 +23,13 @@ EXPORTED = ["pa_cache_append", "pa_attention_workspace_size", "pa_attention", "p
             "pa_workspace_init", "pa_last_error_string", "pa_version",
             "pa_set_kernel_timing_events", "pa_set_prefill_timing_events",
             "pa_attention_noalloc", "pa_copy_blocks", "pa_set_kernel_span_buffer",
-            "pa_set_wait_limit_ns",
+            "pa_set_wait_limit_ns", "pa_attention_key_weights",
+            "pa_attention_key_weights_workspace_size", "pa_evict_keys", "pa_evict_workspace_size",
+            "pa_cache_read",
             "pa_test_skip_one_copy", "pa_selftest_wait_timeout"]
 EXPORTED_BM = ["pa_bm_create", "pa_bm_destroy", "pa_bm_num_free", "pa_bm_append",
                "pa_bm_append_tokens", "pa_bm_fork", "pa_bm_free", "pa_bm_block_table",
-               "pa_bm_num_tokens", "pa_bm_refcount", "pa_bm_cached_prefix"]
+               "pa_bm_num_tokens", "pa_bm_refcount", "pa_bm_cached_prefix", "pa_bm_evict"]
 
 
 class CacheDesc(ctypes.Structure):
@@ -64,6 +67,21 @@ def load() -> ctypes.CDLL:
                                i32, i32, i32, i32, i32, i32, ctypes.c_float, vp, i32, vp,
                                ctypes.c_size_t, vp]
     L.pa_attention.restype = ctypes.c_int
+    L.pa_attention_key_weights_workspace_size.argtypes = [i32] * 8
+    L.pa_attention_key_weights_workspace_size.restype = ctypes.c_size_t
+    L.pa_attention_key_weights.argtypes = [vp, i32, vp, vp, ctypes.POINTER(CacheDesc), i32p, i32,
+                                           i32p, i32p, i32, i32, i32, i32, i32, i32,
+                                           ctypes.c_float, vp, i32, vp, i32p, i32, i32,
+                                           ctypes.c_float, vp, ctypes.c_size_t, vp]
+    L.pa_attention_key_weights.restype = ctypes.c_int
+    L.pa_evict_workspace_size.argtypes = [i32] * 4
+    L.pa_evict_workspace_size.restype = ctypes.c_size_t
+    L.pa_evict_keys.argtypes = [vp, vp, ctypes.POINTER(CacheDesc), i32p, i32p, i32, i32p, i32p,
+                                i32, i32, i32, i32, vp, i32p, i32p, i32, i32, i32p, i32p, vp,
+                                ctypes.c_size_t, vp]
+    L.pa_evict_keys.restype = ctypes.c_int
+    L.pa_cache_read.argtypes = [i64p, i32, vp, vp, ctypes.POINTER(CacheDesc), vp, vp, i32, vp, vp]
+    L.pa_cache_read.restype = ctypes.c_int
     L.pa_attention_noalloc.argtypes = [vp, i32, vp, vp, ctypes.POINTER(CacheDesc), i32p, i32,
                                        i32p, i32p, i32, i32, i32, i32, i32, i32, ctypes.c_float,
                                        vp, i32, vp, vp]
@@ -89,6 +107,8 @@ def load() -> ctypes.CDLL:
     L.pa_bm_free.restype = i32
     L.pa_bm_block_table.argtypes = [vp, i64, vp, i32]
     L.pa_bm_block_table.restype = i32
+    L.pa_bm_evict.argtypes = [vp, i64, i64, vp, i32]
+    L.pa_bm_evict.restype = i32
     L.pa_bm_num_tokens.argtypes = [vp, i64]
     L.pa_bm_num_tokens.restype = i64
     L.pa_bm_refcount.argtypes = [vp, i32]

@@ -88,6 +88,15 @@ class BlockManager:
         self._L.pa_bm_block_table(self._h, int(seq), out.ctypes.data, n)
         return out[:n]
 
+    def evict(self, seq: int, keep: int, width: Optional[int] = None) -> np.ndarray:
+        """Reduce the sequence to `keep` positions; returns its new block table, padded with -1 to
+        `width` entries (evict_keys' dst_tables row beside the table from before the call)."""
+        need = -(-max(int(keep), 0) // self.block_size)
+        out = np.full(max(need, 1) if width is None else int(width), -1, dtype=np.int32)
+        n = self._check(self._L.pa_bm_evict(self._h, int(seq), int(keep), out.ctypes.data,
+                                            int(out.shape[0])))
+        return out[:n] if width is None else out
+
     def num_tokens(self, seq: int) -> int:
         return int(self._check(self._L.pa_bm_num_tokens(self._h, int(seq))))
 

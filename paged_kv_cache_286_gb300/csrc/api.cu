@@ -124,7 +124,7 @@ pa_status check_cache_desc(const pa_cache_desc* c, bool for_attention) {
     return fail(PA_ERR_INVALID_ARG, "cache descriptor has a non-positive size");
   if (c->block_size != pa::kBlockSize)
     return fail(PA_ERR_UNSUPPORTED, "block_size %d is not built (16 is)", c->block_size);
-  if (c->cache_dtype != PA_BF16 && c->cache_dtype != PA_FP8_E4M3)
+  if (c->cache_dtype != PA_BF16 && c->cache_dtype != PA_FP8_E4M3 && c->cache_dtype != PA_MXFP4)
     return fail(PA_ERR_UNSUPPORTED, "cache_dtype %d is not built", c->cache_dtype);
   if (c->cache_dtype == PA_FP8_E4M3 &&
       !(std::isfinite(c->k_scale) && std::isfinite(c->v_scale) && c->k_scale > 0.f &&
@@ -132,6 +132,9 @@ pa_status check_cache_desc(const pa_cache_desc* c, bool for_attention) {
     return fail(PA_ERR_INVALID_ARG, "E4M3 cache needs finite positive k_scale and v_scale");
   if (c->head_dim % 16 != 0)
     return fail(PA_ERR_UNSUPPORTED, "head_dim %d is not a multiple of 16", c->head_dim);
+  if (c->cache_dtype == PA_MXFP4 && c->head_dim != 64 && c->head_dim != 128)
+    return fail(PA_ERR_UNSUPPORTED, "an MXFP4 cache of head_dim %d is not built (64 and 128 are)",
+                c->head_dim);
   if (for_attention) {
     const bool ok = c->cache_dtype == PA_FP8_E4M3 ? c->head_dim == 128
                                                   : (c->head_dim == 64 || c->head_dim == 128);
@@ -145,6 +148,29 @@ pa_status check_cache_desc(const pa_cache_desc* c, bool for_attention) {
     return fail(PA_ERR_INVALID_ARG,
                 "pool too large: %lld rows of (block, kv head, slot), at most 2^31 - 1",
                 static_cast<long long>(rows));
+  return PA_OK;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+// The per-key weights of pa_attention_key_weights and pa_evict_keys.
+pa_status check_weights(const float* key_weights, const int32_t* weight_rows,
+                        int32_t num_weight_rows, int32_t max_keys, int32_t num_seqs,
+                        int32_t max_context_len, bool nothing) {
+  if (num_weight_rows < 0 || max_keys < 0) return fail(PA_ERR_INVALID_ARG, "negative size");
+  if (nothing) return PA_OK;
+  if (!key_weights) return fail(PA_ERR_INVALID_ARG, "key_weights is NULL");
+  if (!aligned(key_weights, 4) || !aligned(weight_rows, 4))
+    return fail(PA_ERR_INVALID_ARG, "misaligned pointer (key_weights or weight_rows)");
+  if (max_keys < max_context_len)
+    return fail(PA_ERR_INVALID_ARG, "key_weights has rows of %d keys, max_context_len is %d",
+                max_keys, max_context_len);
+  if (!weight_rows && num_weight_rows < num_seqs)
+    return fail(PA_ERR_INVALID_ARG, "%d rows of key_weights for %d sequences (and no weight_rows)",
+                num_weight_rows, num_seqs);
   return PA_OK;
 }
 
@@ -200,6 +226,19 @@ WsLayout workspace_layout(int32_t S, int32_t T, int32_t Hq, int32_t Hkv, int32_t
   off = up(off + sizeof(float) * rows * parts);
   w.part_o = off;
   off = up(off + sizeof(float) * rows * parts * size_t(std::max(D, 0)));
+  w.total = off;
+  return w;
+}
+
+KeyWeightsLayout key_weights_layout(int32_t S, int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                                    int32_t max_ctx, int32_t max_q) {
+  KeyWeightsLayout w{};
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  size_t off = up(workspace_layout(S, T, Hq, Hkv, D, max_ctx, max_q).total);
+  w.lse = off;
+  off = up(off + sizeof(float) * size_t(std::max(T, 0)) * size_t(std::max(Hq, 0)));
+  w.chunk_start = off;
+  off = up(off + sizeof(int32_t) * (size_t(std::max(S, 0)) + 1));
   w.total = off;
   return w;
 }
@@ -336,7 +375,8 @@ pa_status pa_check_error(void* workspace, cudaStream_t stream, uint32_t* word_ou
     return fail(PA_ERR_TIMEOUT, "a device-side wait timed out (error word 0x%x)", word);
   if (word)
     return fail(PA_ERR_OUT_OF_RANGE,
-                "device saw an out-of-range block id, slot or length (error word 0x%x)", word);
+                "device saw an out-of-range block id, slot, length or weight row (error word 0x%x)",
+                word);
   return PA_OK;
 }
 
@@ -389,14 +429,16 @@ size_t pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_tokens, int32
       .total;
 }
 
-pa_status pa_attention(const void* q, int32_t num_q_tokens, const void* k_cache,
-                       const void* v_cache, const pa_cache_desc* cache,
-                       const int32_t* block_tables, int32_t max_blocks_per_seq,
-                       const int32_t* context_lens, const int32_t* query_start_loc,
-                       int32_t num_seqs, int32_t max_context_len, int32_t max_query_len,
-                       int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
-                       void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes,
-                       cudaStream_t stream) {
+// Attention of one step; `lse` ([num_q_tokens][num_q_heads], or NULL) also receives the rows'
+// log-sum-exps in the log2 domain.
+static pa_status attend(const void* q, int32_t num_q_tokens, const void* k_cache,
+                        const void* v_cache, const pa_cache_desc* cache,
+                        const int32_t* block_tables, int32_t max_blocks_per_seq,
+                        const int32_t* context_lens, const int32_t* query_start_loc,
+                        int32_t num_seqs, int32_t max_context_len, int32_t max_query_len,
+                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                        void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream, float* lse) {
   bool nothing = false;
   pa_status st = pa::check_attention_args(
       q, num_q_tokens, k_cache, v_cache, cache, block_tables, max_blocks_per_seq, context_lens,
@@ -416,8 +458,10 @@ pa_status pa_attention(const void* q, int32_t num_q_tokens, const void* k_cache,
   // boxes of one or two kv heads' rows (two only for single-token E4M3 decode, where no
   // prefill tile reads these maps)
   const int hpi = pa::decode_heads_per_item(*cache, num_q_heads, num_kv_heads, max_query_len);
-  if ((st = encode_pool_map(&maps.k2, k_cache, *cache, hpi)) != PA_OK) return st;
-  if ((st = encode_pool_map(&maps.v2, v_cache, *cache, hpi)) != PA_OK) return st;
+  if (cache->cache_dtype != PA_MXFP4) {  // (MXFP4 tiles are contiguous: untiled copies)
+    if ((st = encode_pool_map(&maps.k2, k_cache, *cache, hpi)) != PA_OK) return st;
+    if ((st = encode_pool_map(&maps.v2, v_cache, *cache, hpi)) != PA_OK) return st;
+  }
 
   const int32_t G = num_q_heads / num_kv_heads;
   const bool use_prefill = pa::prefill_path_enabled(*cache, num_q_heads, num_kv_heads) &&
@@ -444,8 +488,199 @@ pa_status pa_attention(const void* q, int32_t num_q_tokens, const void* k_cache,
   a.wait_ns = g_wait_ns;
   a.skip_copy = g_skip_copy;
   a.span = g_span;
+  a.lse = lse;
   cudaError_t e = pa::launch_attention(a, ws, maps, use_prefill, g_before, g_after);
   if (e != cudaSuccess) return cuda_fail(e, "pa_attention launch");
+  return PA_OK;
+}
+
+
+pa_status pa_attention(const void* q, int32_t num_q_tokens, const void* k_cache,
+                       const void* v_cache, const pa_cache_desc* cache,
+                       const int32_t* block_tables, int32_t max_blocks_per_seq,
+                       const int32_t* context_lens, const int32_t* query_start_loc,
+                       int32_t num_seqs, int32_t max_context_len, int32_t max_query_len,
+                       int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                       void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream) {
+  return attend(q, num_q_tokens, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
+                context_lens, query_start_loc, num_seqs, max_context_len, max_query_len,
+                num_q_heads, num_kv_heads, head_dim, scale, out, out_dtype, workspace,
+                workspace_bytes, stream, nullptr);
+}
+
+size_t pa_attention_key_weights_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
+                                               int32_t num_q_heads, int32_t num_kv_heads,
+                                               int32_t head_dim, int32_t block_size,
+                                               int32_t max_context_len, int32_t max_query_len) {
+  (void)block_size;
+  return pa::key_weights_layout(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
+                                max_context_len, max_query_len)
+      .total;
+}
+
+pa_status pa_attention_key_weights(
+    const void* q, int32_t num_q_tokens, const void* k_cache, const void* v_cache,
+    const pa_cache_desc* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
+    int32_t max_context_len, int32_t max_query_len, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, float scale, void* out, int32_t out_dtype, float* key_weights,
+    const int32_t* weight_rows, int32_t num_weight_rows, int32_t max_keys, float decay,
+    void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  bool nothing = false;
+  pa_status st = pa::check_attention_args(
+      q, num_q_tokens, k_cache, v_cache, cache, block_tables, max_blocks_per_seq, context_lens,
+      query_start_loc, num_seqs, max_context_len, max_query_len, num_q_heads, num_kv_heads,
+      head_dim, scale, out, out_dtype, &nothing);
+  if (st != PA_OK) return st;
+  if ((st = check_weights(key_weights, weight_rows, num_weight_rows, max_keys, num_seqs,
+                          max_context_len, nothing)) != PA_OK)
+    return st;
+  if (!(std::isfinite(decay) && decay >= 0.f))
+    return fail(PA_ERR_INVALID_ARG, "decay must be finite and not negative");
+  if (!workspace) return fail(PA_ERR_INVALID_ARG, "workspace is NULL");
+  if (nothing) return PA_OK;
+  const pa::KeyWeightsLayout ws =
+      pa::key_weights_layout(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
+                             max_context_len, max_query_len);
+  if (workspace_bytes < ws.total)
+    return fail(PA_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes,
+                ws.total);
+  uint8_t* wsb = static_cast<uint8_t*>(workspace);
+  float* lse = reinterpret_cast<float*>(wsb + ws.lse);
+  st = attend(q, num_q_tokens, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
+              context_lens, query_start_loc, num_seqs, max_context_len, max_query_len, num_q_heads,
+              num_kv_heads, head_dim, scale, out, out_dtype, workspace, workspace_bytes, stream,
+              lse);
+  if (st != PA_OK) return st;
+  pa::KeyWeightsArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k_cache = static_cast<const uint8_t*>(k_cache);
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.qsl = query_start_loc;
+  a.lse = lse;
+  a.weight_rows = weight_rows;
+  a.key_weights = key_weights;
+  a.chunk_start = reinterpret_cast<int32_t*>(wsb + ws.chunk_start);
+  a.err = static_cast<uint32_t*>(workspace);
+  a.num_seqs = num_seqs;
+  a.num_blocks = cache->num_blocks;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.max_context_len = max_context_len;
+  a.max_query_len = max_query_len;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.cache_dtype = cache->cache_dtype;
+  a.num_weight_rows = num_weight_rows;
+  a.max_keys = max_keys;
+  a.score_log2 =
+      scale * 1.4426950408889634f * (cache->cache_dtype == PA_FP8_E4M3 ? cache->k_scale : 1.f);
+  a.decay = decay;
+  const cudaError_t e = pa::launch_key_weights(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "pa_attention_key_weights launch");
+  return PA_OK;
+}
+
+size_t pa_evict_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t max_context_len,
+                               int32_t max_keep_len) {
+  (void)num_seqs;
+  (void)num_kv_heads;
+  (void)max_context_len;
+  (void)max_keep_len;
+  return PA_WORKSPACE_HEADER_BYTES;
+}
+
+pa_status pa_evict_keys(void* k_cache, void* v_cache, const pa_cache_desc* cache,
+                        const int32_t* block_tables, const int32_t* dst_tables,
+                        int32_t max_blocks_per_seq, const int32_t* context_lens,
+                        const int32_t* keep_lens, int32_t num_seqs, int32_t max_context_len,
+                        int32_t max_keep_len, int32_t recent, float* key_weights,
+                        const int32_t* weight_rows, const int32_t* dst_weight_rows,
+                        int32_t num_weight_rows, int32_t max_keys, int32_t* kept,
+                        int32_t* new_lens, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream) {
+  g_last_error.clear();
+  if (num_seqs < 0 || max_keep_len < 0 || recent < 0)
+    return fail(PA_ERR_INVALID_ARG, "negative size");
+  pa_status st = check_cache_desc(cache, false);
+  if (st != PA_OK) return st;
+  const bool nothing = num_seqs == 0;
+  if (!nothing && max_context_len <= 0)
+    return fail(PA_ERR_INVALID_ARG, "max_context_len must be positive");
+  if ((st = check_weights(key_weights, weight_rows, num_weight_rows, max_keys, num_seqs,
+                          max_context_len, nothing)) != PA_OK)
+    return st;
+  if (!workspace) return fail(PA_ERR_INVALID_ARG, "workspace is NULL");
+  if (workspace_bytes < pa_evict_workspace_size(num_seqs, cache->num_kv_heads, max_context_len,
+                                                max_keep_len))
+    return fail(PA_ERR_INVALID_ARG, "workspace too small: %zu bytes", workspace_bytes);
+  if (nothing) return PA_OK;
+  if (!k_cache || !v_cache || !block_tables || !context_lens || !keep_lens || !new_lens ||
+      (!kept && max_keep_len > 0))
+    return fail(PA_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (max_blocks_per_seq <= 0)
+    return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq must be positive");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_tables, 4) ||
+      !aligned(dst_tables, 4) || !aligned(context_lens, 4) || !aligned(keep_lens, 4) ||
+      !aligned(dst_weight_rows, 4) || !aligned(kept, 4) || !aligned(new_lens, 4) ||
+      !aligned(workspace, 4))
+    return fail(PA_ERR_INVALID_ARG, "misaligned pointer (caches need 16 bytes)");
+  // every (sequence, kv head) reads the lengths while the new ones are written
+  const size_t lens_bytes = sizeof(int32_t) * static_cast<size_t>(num_seqs);
+  for (const int32_t* in : {context_lens, keep_lens, weight_rows, dst_weight_rows})
+    if (in && overlap(in, lens_bytes, new_lens, lens_bytes))
+      return fail(PA_ERR_INVALID_ARG, "new_lens overlaps an input");
+  pa::EvictArgs a{};
+  a.k_cache = static_cast<uint8_t*>(k_cache);
+  a.v_cache = static_cast<uint8_t*>(v_cache);
+  a.block_tables = block_tables;
+  a.dst_tables = dst_tables ? dst_tables : block_tables;
+  a.context_lens = context_lens;
+  a.keep_lens = keep_lens;
+  a.key_weights = key_weights;
+  a.weight_rows = weight_rows;
+  a.dst_weight_rows = dst_weight_rows;
+  a.kept = kept;
+  a.new_lens = new_lens;
+  a.err = static_cast<uint32_t*>(workspace);
+  a.num_seqs = num_seqs;
+  a.num_blocks = cache->num_blocks;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.head_dim = cache->head_dim;
+  a.cache_dtype = cache->cache_dtype;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.max_context_len = max_context_len;
+  a.max_keep_len = max_keep_len;
+  a.recent = recent;
+  a.num_weight_rows = num_weight_rows;
+  a.max_keys = max_keys;
+  const cudaError_t e = pa::launch_evict(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "pa_evict_keys launch");
+  return PA_OK;
+}
+
+pa_status pa_cache_read(const int64_t* slot_mapping, int32_t num_tokens, const void* k_cache,
+                        const void* v_cache, const pa_cache_desc* cache, void* k, void* v,
+                        int32_t out_dtype, void* workspace, cudaStream_t stream) {
+  g_last_error.clear();
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens < 0");
+  pa_status st = check_cache_desc(cache, false);
+  if (st != PA_OK) return st;
+  if (out_dtype != PA_FP32 && out_dtype != PA_BF16)
+    return fail(PA_ERR_UNSUPPORTED, "out_dtype %d is not built", out_dtype);
+  if (!workspace) return fail(PA_ERR_INVALID_ARG, "workspace is NULL");
+  if (num_tokens == 0) return PA_OK;
+  if (!k || !v || !slot_mapping || !k_cache || !v_cache)
+    return fail(PA_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(slot_mapping, 8) || !aligned(workspace, 4))
+    return fail(PA_ERR_INVALID_ARG, "misaligned pointer (k, v and caches need 16 bytes)");
+  const cudaError_t e =
+      pa::launch_cache_read(slot_mapping, num_tokens, k_cache, v_cache, *cache, k, v,
+                            out_dtype == PA_BF16, static_cast<uint32_t*>(workspace), stream);
+  if (e != cudaSuccess) return cuda_fail(e, "pa_cache_read launch");
   return PA_OK;
 }
 

@@ -251,6 +251,41 @@ int32_t pa_bm_free(pa_block_manager* bm, int64_t seq) {
   return 0;
 }
 
+int32_t pa_bm_evict(pa_block_manager* bm, int64_t seq, int64_t keep, int32_t* table_out,
+                    int32_t cap) {
+  if (!bm || keep < 0 || cap < 0 || (cap > 0 && !table_out)) return PA_BM_BAD_ARG;
+  auto it = bm->seqs.find(seq);
+  if (it == bm->seqs.end() || keep > it->second.ntok) return PA_BM_BAD_ARG;
+  Seq& s = it->second;
+  const int64_t nblk = (keep + bm->bs - 1) / bm->bs;
+  if (nblk > cap) return PA_BM_BAD_ARG;
+  if (keep < s.ntok) {
+    int32_t shared = 0;
+    for (int64_t i = 0; i < nblk; ++i) shared += bm->ref[s.blocks[i]] > 1;
+    // fresh blocks come first: the released ones still hold keys that are to be moved
+    if (shared > bm->available()) return PA_BM_NO_SPACE;
+    for (int64_t i = 0; i < nblk; ++i) {
+      const int32_t b = s.blocks[i];
+      if (bm->ref[b] > 1) {
+        s.blocks[i] = bm->take();
+        bm->drop(b);
+      } else if (bm->hashed[b]) {
+        auto h = bm->by_hash.find(bm->block_hash[b]);
+        if (h != bm->by_hash.end() && h->second == b) bm->by_hash.erase(h);
+        bm->hashed[b] = 0;
+        bm->block_tokens[b].clear();
+      }
+    }
+    for (size_t i = static_cast<size_t>(nblk); i < s.blocks.size(); ++i) bm->drop(s.blocks[i]);
+    s.blocks.resize(static_cast<size_t>(nblk));
+    s.ntok = keep;
+    s.hashing = false;
+    s.tail.clear();
+  }
+  for (int64_t i = 0; i < cap; ++i) table_out[i] = i < nblk ? s.blocks[i] : -1;
+  return static_cast<int32_t>(nblk);
+}
+
 int32_t pa_bm_block_table(const pa_block_manager* bm, int64_t seq, int32_t* table_out,
                           int32_t cap) {
   if (!bm) return PA_BM_BAD_ARG;

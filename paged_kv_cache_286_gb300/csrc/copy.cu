@@ -38,8 +38,11 @@ cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, const pa_cache_desc
                                const int32_t* pairs, int32_t num_pairs, uint32_t* err,
                                cudaStream_t stream) {
   if (num_pairs == 0) return cudaSuccess;
-  const int64_t bytes = static_cast<int64_t>(c.num_kv_heads) * c.block_size * c.head_dim *
-                        (c.cache_dtype == PA_FP8_E4M3 ? 1 : 2);
+  const int64_t bytes =
+      c.cache_dtype == PA_MXFP4
+          ? static_cast<int64_t>(c.num_kv_heads) * (c.head_dim * 17 / 2)
+          : static_cast<int64_t>(c.num_kv_heads) * c.block_size * c.head_dim *
+                (c.cache_dtype == PA_FP8_E4M3 ? 1 : 2);
   const int64_t vecs = bytes / 16;
   const int64_t per_cta = 256;
   const unsigned gx = static_cast<unsigned>(std::min<int64_t>((vecs + per_cta - 1) / per_cta, 64));

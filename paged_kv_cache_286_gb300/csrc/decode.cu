@@ -35,74 +35,11 @@
 #include <climits>
 #include <utility>
 
+#include "decode_items.cuh"
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
 namespace pa {
-
-struct DecodeParams {
-  const __nv_bfloat16* q;
-  const int32_t* block_tables;
-  const int32_t* context_lens;
-  const int32_t* qsl;
-  int32_t* item_start;
-  int32_t* pf_item_start;  // [S+1] prefill item prefix sums over the runs in claim order
-  int32_t* pf_order;       // [S] the runs with prefill items, longest item first
-  int32_t* merge_start;    // [S+1] prefix sums of the rows the merge combines
-  float* part_lse;
-  float* part_o;
-  void* out;
-  WsHeader* hdr;
-  int32_t max_blocks_per_seq;
-  int32_t num_seqs;
-  int32_t num_q_heads;
-  int32_t num_kv_heads;
-  int32_t group;           // q heads per kv head
-  int32_t num_blocks;
-  int32_t max_context_len;
-  int32_t max_query_len;
-  int32_t pblk;
-  int32_t pmax;
-  int32_t decode_max_query;  // longer query runs go to the prefill-tile path
-  int32_t decode_max_rows;   // so do runs of more (token x head) rows than one decode tile
-  int32_t rows_per_tile;   // 8 * RT of the decode kernel instance
-  int32_t heads_per_item;  // HPI of the decode kernel instance
-  int32_t out_bf16;
-  float score_log2;        // scale * log2(e) (* k_scale for E4M3)
-  float v_out_scale;       // v_scale for E4M3, else 1
-  uint64_t* span;          // benchmark hook: [first CTA start, last CTA end] in ns, or NULL
-  int32_t wait_at_end;     // launched after the prefill kernel: wait for it only at the end
-  int32_t sms;             // SMs of the device (the plan's SM split)
-  int32_t kv_tile_bytes;   // bytes of one (block, kv head) tile of K plus V
-  uint64_t wait_ns;        // limit of every bounded wait
-  int32_t skip_copy;       // test hook: item 0 leaves out its first tile copy (see pa.h)
-};
-
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-// Partitions of a decode-path sequence of L keys.
-__device__ __forceinline__ int partitions_of(const DecodeParams& p, int L) {
-  return ceil_div(ceil_div(L, kBlockSize), p.pblk);
-}
-
-// Items of one sequence on the decode path (0 if it belongs to the prefill path or is invalid).
-__device__ __forceinline__ int decode_items_of(const DecodeParams& p, int n, int L, bool* bad) {
-  *bad = false;
-  if (n <= 0) {
-    *bad = (n < 0);
-    return 0;
-  }
-  if (n > L || L > p.max_context_len || n > p.max_query_len ||
-      L > p.max_blocks_per_seq * kBlockSize) {
-    *bad = true;
-    return 0;
-  }
-  if (n > p.decode_max_query || n * p.group > p.decode_max_rows) return 0;
-  const int tpt = p.rows_per_tile / (p.group * p.heads_per_item);  // query tokens per tile
-  const int qtiles = ceil_div(n, tpt);
-  const int nparts = partitions_of(p, L);
-  return p.num_kv_heads / p.heads_per_item * qtiles * nparts;
-}
 
 // Prefill-path items of one sequence: one per (kv head, 128-row tile of tokens x heads, key
 // split of the tile).
@@ -408,10 +345,6 @@ constexpr int decode_smem_bytes() {
          kDecodeWarps * NST * 8 /*mbarriers*/ + 2 * 64 /*item slots*/;
 }
 
-struct ItemInfo {
-  int s, h, qt, part, t0, n, L, nparts, blk_begin, blk_end, pos_base, rows, valid, idx;
-};
-
 // Instances with 2-stage rings are held to 3 CTAs per SM (at most 170 registers a thread): the
 // kernel is latency-bound per SM, and the third CTA's warps, which the smaller rings leave room
 // for in shared memory, keep more blocks in flight.
@@ -463,44 +396,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, NST == 2 ? 3 : 1)
 
   // Thread 0 claims and decodes the CTA's next item while the current one streams, so the
   // atomic and the search over item_start stay off the critical path.
-  auto fetch_item = [&](ItemInfo* dst) {
-    ItemInfo info;
-    const int item = static_cast<int>(atomicAdd(&p.hdr->decode_counter, 1u));
-    info.valid = item < total_items;
-    info.idx = item;
-    if (info.valid) {
-      int lo = 0, hi = p.num_seqs;  // largest s with item_start[s] <= item
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.item_start[mid] <= item) lo = mid; else hi = mid;
-      }
-      const int s = lo;
-      const int t0 = p.qsl[s];
-      const int n = p.qsl[s + 1] - t0;
-      const int L = p.context_lens[s];
-      const int tpt = R / (p.group * HPI);
-      const int istart = p.item_start[s];
-      const int qtiles = ceil_div(n, tpt);
-      const int nblk = ceil_div(L, kBlockSize);
-      const int nparts = ceil_div(nblk, p.pblk);
-      int local = item - istart;
-      const int part = local % nparts;
-      local /= nparts;
-      const int qt = local % qtiles;
-      const int h = (local / qtiles) * HPI;                // first kv head of the item
-      const int tok_begin = qt * tpt;
-      const int tok_end = min(n, tok_begin + tpt);
-      const int pos_max = L - n + tok_end - 1;           // last position in the tile
-      const int blk_tile = pos_max / kBlockSize + 1;     // blocks the tile can see
-      info.s = s; info.h = h; info.qt = qt; info.part = part; info.t0 = t0 + tok_begin;
-      info.n = tok_end - tok_begin; info.L = L; info.nparts = nparts;
-      info.blk_begin = min(part * p.pblk, blk_tile);
-      info.blk_end = min((part + 1) * p.pblk, blk_tile);
-      info.pos_base = L - n + tok_begin;                 // position of the tile's first token
-      info.rows = info.n * p.group * HPI;
-    }
-    *dst = info;
-  };
+  auto fetch_item = [&](ItemInfo* dst) { *dst = claim_item<R, HPI>(p, total_items); };
   if (threadIdx.x == 0) fetch_item(&s_item[0]);
   int cur = 0;
 
@@ -885,6 +781,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, NST == 2 ? 3 : 1)
           reinterpret_cast<__nv_bfloat16*>(p.out)[orow * D + d] = __float2bfloat16_rn(val);
         else
           reinterpret_cast<float*>(p.out)[orow * D + d] = val;
+        if (p.lse && d == 0)
+          p.lse[orow] = Lsum == 0.f ? -CUDART_INF_F : M + __log2f(Lsum);
       } else {
         const int64_t prow = orow * p.pmax + I.part;
         p.part_o[prow * D + d] = val;
@@ -992,6 +890,7 @@ __device__ __forceinline__ void merge_row(const DecodeParams& p, int64_t rid, in
 #pragma unroll
   for (int o = 16; o; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  if (p.lse && lane == 0) p.lse[rid] = wsum == 0.f ? -CUDART_INF_F : M + __log2f(wsum);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int64_t o = rid * D + lane * kPer + i;
@@ -1040,6 +939,21 @@ __global__ void __launch_bounds__(256, 4) merge_kernel(const DecodeParams p) {
   }
 }
 
+// The merge of the call's split rows: at most one resident wave of 8-warp CTAs (the merge rows
+// are fewer than all rows).
+template <int D>
+static cudaError_t run_merge(const AttnArgs& a, const DecodeParams& p) {
+  LaunchInfo mi;
+  cudaError_t e = launch_info(merge_kernel<D>, 256, 0, &mi);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(a.num_q_tokens) * a.num_q_heads;
+  const int64_t blocks = std::min<int64_t>((rows + 7) / 8, int64_t(mi.sms) * mi.per_sm);
+  if (blocks > 0)
+    e = launch_dependent(merge_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                         a.stream, p);
+  return e;
+}
+
 template <int D, bool kFp8, int NST, int RT, int HPI = 1>
 static cudaError_t run_decode(const AttnArgs& a, const WsLayout& ws, const DecodeParams& p,
                               const CUtensorMap& kmap, const CUtensorMap& vmap,
@@ -1059,17 +973,6 @@ static cudaError_t run_decode(const AttnArgs& a, const WsLayout& ws, const Decod
   e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kDecodeWarps * 32), smem,
                        a.stream, kmap, vmap, p);
   if (after) cudaEventRecord(after, a.stream);
-  if (e != cudaSuccess) return e;
-  if (ws.pmax > 1) {
-    // at most one resident wave of 8-warp CTAs; the merge rows are fewer than all rows
-    LaunchInfo mi;
-    if ((e = launch_info(merge_kernel<D>, 256, 0, &mi)) != cudaSuccess) return e;
-    const int64_t rows = static_cast<int64_t>(a.num_q_tokens) * a.num_q_heads;
-    const int64_t blocks = std::min<int64_t>((rows + 7) / 8, int64_t(mi.sms) * mi.per_sm);
-    if (blocks > 0)
-      e = launch_dependent(merge_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                           a.stream, p);
-  }
   return e;
 }
 
@@ -1121,11 +1024,13 @@ cudaError_t launch_attention(const AttnArgs& a, const WsLayout& ws, const PoolMa
   // workspace, sized for the bf16 choice, then holds fewer partitions than it has room for;
   // pmax stays the row stride of the partial arrays).  Fewer, longer partitions also make the
   // merge cheaper.
+  // A 4-bit block is a quarter of the bytes, and its items take up to four times the blocks.
   const bool fp8_cache = a.cache.cache_dtype == PA_FP8_E4M3;
+  const bool mx = a.cache.cache_dtype == PA_MXFP4;
   const int hpi = decode_heads_per_item(a.cache, a.num_q_heads, a.num_kv_heads,
                                         a.max_query_len);
   p.heads_per_item = hpi;
-  p.pblk = (fp8_cache && ws.pblk <= 32) ? ws.pblk * 2 : ws.pblk;
+  p.pblk = ((fp8_cache || mx) && ws.pblk <= 32) ? ws.pblk * 2 : ws.pblk;
   // a warp holds the table entries of its blocks of a partition one per lane
   if (p.pblk > kDecodeWarps * 32) return cudaErrorInvalidValue;
   p.pmax = ws.pmax;
@@ -1147,13 +1052,14 @@ cudaError_t launch_attention(const AttnArgs& a, const WsLayout& ws, const PoolMa
   const int dec_q = std::min(a.max_query_len, p.decode_max_query);
   const bool mixed = prefill && routes_to_prefill(a.max_query_len, p.group);
   const bool rt2 = p.group > 8 || (!mixed && static_cast<int64_t>(dec_q) * p.group > 8);
-  p.rows_per_tile = rt2 ? 16 : 8;
+  p.rows_per_tile = mx ? 8 * mx_row_tiles(a.max_query_len, p.group) : rt2 ? 16 : 8;
+  p.lse = a.lse;
 
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p.sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  p.kv_tile_bytes = 2 * kBlockSize * a.head_dim * (fp8 ? 1 : 2);
+  p.kv_tile_bytes = mx ? 2 * a.head_dim * 17 / 2 : 2 * kBlockSize * a.head_dim * (fp8 ? 1 : 2);
   p.span = a.span;
 
   e = launch_dependent(plan_kernel, dim3(1), dim3(1024), 0, a.stream, p);
@@ -1171,7 +1077,11 @@ cudaError_t launch_attention(const AttnArgs& a, const WsLayout& ws, const PoolMa
       return e;
     p.wait_at_end = 1;
   }
-  if (fp8 && hpi == 2)
+  if (mx) {
+    if (before) cudaEventRecord(before, a.stream);
+    e = launch_decode_mx(a, p.pmax, p);
+    if (after) cudaEventRecord(after, a.stream);
+  } else if (fp8 && hpi == 2)
     e = run_decode<128, true, 2, 1, 2>(a, ws, p, kmap, vmap, before, after);
   else if (fp8)
     e = rt2 ? run_decode<128, true, 4, 2>(a, ws, p, kmap, vmap, before, after)
@@ -1182,7 +1092,8 @@ cudaError_t launch_attention(const AttnArgs& a, const WsLayout& ws, const PoolMa
   else
     e = rt2 ? run_decode<64, false, 4, 2>(a, ws, p, kmap, vmap, before, after)
             : run_decode<64, false, 4, 1>(a, ws, p, kmap, vmap, before, after);
-  return e;
+  if (e != cudaSuccess || ws.pmax <= 1) return e;
+  return a.head_dim == 128 ? run_merge<128>(a, p) : run_merge<64>(a, p);
 }
 
 }  // namespace pa

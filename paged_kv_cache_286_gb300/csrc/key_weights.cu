@@ -1,0 +1,270 @@
+// Accumulated attention weight of every cached key, for eviction by weight.
+//
+// What it computes, after the attention of the step has left each row's log-sum-exp (a row is a
+// query token and q head): for every key j of a sequence with query tokens, per kv head,
+//   W[j] <- decay * W[j] + sum over the rows that see j of 2^(s_j - lse_row),
+// s_j = scale * log2(e) * q . k_j, i.e. the sum of the softmax weights that j received.
+//
+//  * The keys stay: a warp holds 32 keys of one kv head as MMA fragments (M = keys, two m16 tiles)
+//    and the rows of the group pass through shared memory as the N operand, eight at a time, so
+//    a key's sum over rows stays in the lanes that own it and is written once, in a fixed order:
+//    no atomics, the same bits every time.  Keys are read once, whatever the number of rows.
+//  * The log-sum-exp is known, so there is no running maximum: a score costs one FMA, one 2^x and
+//    one add.
+//  * Every pool type becomes bf16 fragments, exactly (E4M3 has four significant bits, E2M1 times
+//    a power of two has two), so q is used as it is and the loop over the rows is the same.
+#include <math_constants.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "mxfp4.cuh"
+#include "pa_common.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kKwWarps = 4;
+constexpr int kKwKeys = 32 * kKwWarps;  // keys of an item
+constexpr int kKwRows = 64;             // rows staged in shared memory at a time
+
+enum class Pool { kBf16, kE4m3, kMx };
+
+// Items of a sequence: its key chunks (for each kv head), none when it does not accumulate.
+__device__ __forceinline__ int kw_chunks(const KeyWeightsArgs& a, int s, uint32_t* err_bits) {
+  const int n = a.qsl[s + 1] - a.qsl[s], L = a.context_lens[s];
+  // (what the attention's plan flags and skips is skipped here too)
+  if (n <= 0 || n > L || L > a.max_context_len || n > a.max_query_len ||
+      L > a.max_blocks_per_seq * kBlockSize)
+    return 0;
+  const int row = a.weight_rows ? a.weight_rows[s] : s;
+  if (row < 0) return 0;
+  if (row >= a.num_weight_rows) {
+    *err_bits |= PA_DEVERR_WEIGHT_ROW;
+    return 0;
+  }
+  return (L + kKwKeys - 1) / kKwKeys;
+}
+
+// One CTA: exclusive prefix sums of the sequences' chunks.
+__global__ void __launch_bounds__(1024) kw_plan_kernel(const KeyWeightsArgs a) {
+  grid_dependency_wait();
+  __shared__ int warp_sums[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int carry = 0;
+  uint32_t bits = 0;
+  for (int base = 0; base < a.num_seqs; base += 1024) {
+    const int s = base + tid;
+    const int c = s < a.num_seqs ? kw_chunks(a, s, &bits) : 0;
+    int x = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+      int w = warp_sums[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+      }
+      warp_sums[lane] = w;
+    }
+    __syncthreads();
+    if (s < a.num_seqs) a.chunk_start[s] = carry + (warp ? warp_sums[warp - 1] : 0) + x - c;
+    carry += warp_sums[31];
+    __syncthreads();
+  }
+  if (tid == 0) a.chunk_start[a.num_seqs] = carry;
+  if (bits) set_error(a.err, bits);
+}
+
+template <Pool kPool, int D>
+__global__ void __launch_bounds__(kKwWarps * 32, 4) key_weights_kernel(const KeyWeightsArgs a) {
+  constexpr int KS = D / 16;               // MMA k-steps
+  constexpr int NC = D / 32;               // 16-byte pieces of 8 dims that a lane has of a row
+  constexpr int kStride = D * 2 + 64;      // bytes of a staged row (two rows: all 32 banks)
+  __shared__ __align__(16) uint8_t s_q[kKwRows * kStride];
+  __shared__ float s_lse[kKwRows];
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int quad = lane >> 2, qc = lane & 3;
+  const int total = a.chunk_start[a.num_seqs];
+  const int G = a.num_q_heads / a.num_kv_heads;
+
+  for (int64_t item = blockIdx.x; item < static_cast<int64_t>(total) * a.num_kv_heads;
+       item += gridDim.x) {
+    const int chunk_id = static_cast<int>(item / a.num_kv_heads);
+    const int h = static_cast<int>(item - static_cast<int64_t>(chunk_id) * a.num_kv_heads);
+    int lo = 0, hi = a.num_seqs;  // largest s with chunk_start[s] <= chunk_id
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.chunk_start[mid] <= chunk_id) lo = mid; else hi = mid;
+    }
+    const int s = lo;
+    const int t0 = a.qsl[s], n = a.qsl[s + 1] - t0, L = a.context_lens[s];
+    const int base = (chunk_id - a.chunk_start[s]) * kKwKeys;  // first key of the item
+    const int key_w = base + 32 * warp;                         // first key of the warp
+
+    // ---- this lane's dims of its four keys as bf16 MMA fragments (A operand): keys
+    // key_w + 16 m + quad (+ 8); of piece c the dims 32 c + 8 qc .. + 7 --------------------
+    uint32_t kf[2][KS][4];
+    float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // [m][i]
+    bool there[2][2];  // keys of bad blocks, which the attention leaves out, receive nothing
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int key = key_w + 16 * m + quad + 8 * i;
+        int phys = -1;
+        if (key < L) {
+          phys = __ldg(a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq +
+                       key / kBlockSize);
+          if (phys >= a.num_blocks) phys = -1;  // (flagged by the attention)
+        }
+        there[m][i] = phys >= 0;
+        const int64_t tile = static_cast<int64_t>(phys) * a.num_kv_heads + h;
+        const int off = key % kBlockSize;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          uint32_t w[4] = {0u, 0u, 0u, 0u};  // 8 dims as bf16 pairs
+          if (phys >= 0) {
+            if constexpr (kPool == Pool::kBf16) {
+              const uint4 x = __ldg(reinterpret_cast<const uint4*>(
+                  a.k_cache + ((tile * kBlockSize + off) * D + 32 * c + 8 * qc) * 2));
+              w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+            } else if constexpr (kPool == Pool::kE4m3) {
+              const uint2 x = __ldg(reinterpret_cast<const uint2*>(
+                  a.k_cache + (tile * kBlockSize + off) * D + 32 * c + 8 * qc));
+              const uint32_t u[2] = {x.x, x.y};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float f0, f1;
+                e4m3x2_to_f32x2(static_cast<uint16_t>(u[j >> 1] >> (16 * (j & 1))), f0, f1);
+                w[j] = pack_bf16x2(f0, f1);
+              }
+            } else {
+              const uint8_t* t = a.k_cache + tile * Mx<D>::kTileBytes;
+              const uint16_t* src = reinterpret_cast<const uint16_t*>(t + off * Mx<D>::kRowBytes);
+              const uint32_t codes =
+                  __ldg(src + 2 * qc * NC + c) |
+                  (static_cast<uint32_t>(__ldg(src + (2 * qc + 1) * NC + c)) << 16);
+              const float sc = e8m0_to_f32(__ldg(t + Mx<D>::kCodeBytes + off * NC + c), 0);
+              uint32_t f[4];
+              e2m1x8_to_f16x2x4(codes, f);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&f[j]));
+                w[j] = pack_bf16x2(y.x * sc, y.y * sc);
+              }
+            }
+          }
+          // k-step 2 c: dims 0 1 (k = 2 qc) and 2 3 (k = 2 qc + 8); k-step 2 c + 1: 4 5 and 6 7
+          kf[m][2 * c][i] = w[0];
+          kf[m][2 * c][2 + i] = w[1];
+          kf[m][2 * c + 1][i] = w[2];
+          kf[m][2 * c + 1][2 + i] = w[3];
+        }
+      }
+
+    // ---- the rows of the tokens that see some key of the item -----------------------------
+    const int first_tok = max(0, base - (L - n));
+    const int rows = (n - first_tok) * G;
+    for (int r0 = 0; r0 < rows; r0 += kKwRows) {
+      const int nr = min(kKwRows, rows - r0);
+      __syncthreads();  // the rows before are read
+      for (int e = threadIdx.x; e < kKwRows * (D / 8); e += kKwWarps * 32) {
+        const int r = e / (D / 8), c = e - r * (D / 8);
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (r < nr) {
+          const int tok = t0 + first_tok + (r0 + r) / G;
+          x = __ldg(reinterpret_cast<const uint4*>(
+              a.q + (static_cast<int64_t>(tok) * a.num_q_heads + h * G + (r0 + r) % G) * D + 8 * c));
+        }
+        *reinterpret_cast<uint4*>(s_q + r * kStride + 16 * c) = x;
+      }
+      for (int r = threadIdx.x; r < kKwRows; r += kKwWarps * 32)
+        s_lse[r] = r < nr ? a.lse[static_cast<int64_t>(t0 + first_tok + (r0 + r) / G) *
+                                      a.num_q_heads + h * G + (r0 + r) % G]
+                          : CUDART_INF_F;  // 2^(0 - inf) = 0
+      __syncthreads();
+      for (int rt = 0; rt < nr; rt += 8) {
+        float acc[2][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(s_q + (rt + quad) * kStride + 64 * c + 16 * qc);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            mma_bf16(acc[m], kf[m][2 * c], x.x, x.y);
+            mma_bf16(acc[m], kf[m][2 * c + 1], x.z, x.w);
+          }
+        }
+        // position of the tile's first row: rows that do not see a key add nothing to it
+        const int pos0 = L - n + first_tok + (r0 + rt) / G;
+        const bool all = key_w + 31 <= pos0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float lse = s_lse[rt + 2 * qc + j];
+          const int pos = all ? INT_MAX
+                              : (rt + 2 * qc + j < nr
+                                     ? L - n + first_tok + (r0 + rt + 2 * qc + j) / G : -1);
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float w = fast_exp2(fmaf(acc[m][2 * i + j], a.score_log2, -lse));
+              if (key_w + 16 * m + quad + 8 * i <= pos) sum[m][i] += w;
+            }
+        }
+      }
+    }
+    // ---- sums over the four lanes of a key, and the update --------------------------------
+    const int64_t row = a.weight_rows ? a.weight_rows[s] : s;
+    float* W = a.key_weights + (row * a.num_kv_heads + h) * static_cast<int64_t>(a.max_keys);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = sum[m][i];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        const int key = key_w + 16 * m + quad + 8 * i;
+        if (qc == 0 && key < L) W[key] = fmaf(a.decay, W[key], there[m][i] ? x : 0.f);
+      }
+    __syncthreads();
+  }
+}
+
+template <Pool kPool, int D>
+cudaError_t run_key_weights(const KeyWeightsArgs& a, cudaStream_t stream) {
+  auto kern = key_weights_kernel<kPool, D>;
+  LaunchInfo li;
+  cudaError_t e = launch_info(kern, kKwWarps * 32, 0, &li);
+  if (e != cudaSuccess) return e;
+  const int64_t upper = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads *
+                        ((a.max_context_len + int64_t(kKwKeys) - 1) / kKwKeys);
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(upper, int64_t(li.sms) * li.per_sm));
+  return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kKwWarps * 32), 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t stream) {
+  cudaError_t e = launch_dependent(kw_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  if (a.cache_dtype == PA_FP8_E4M3) return run_key_weights<Pool::kE4m3, 128>(a, stream);
+  if (a.cache_dtype == PA_MXFP4)
+    return a.head_dim == 128 ? run_key_weights<Pool::kMx, 128>(a, stream)
+                             : run_key_weights<Pool::kMx, 64>(a, stream);
+  return a.head_dim == 128 ? run_key_weights<Pool::kBf16, 128>(a, stream)
+                           : run_key_weights<Pool::kBf16, 64>(a, stream);
+}
+
+}  // namespace pa

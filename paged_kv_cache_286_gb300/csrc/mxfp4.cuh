@@ -1,0 +1,78 @@
+// MXFP4 pool tiles: E2M1 codes (sign, two exponent bits, one mantissa bit: 0 .5 1 1.5 2 3 4 6) in
+// blocks of 32 dims of a row that share one E8M0 scale byte e, which stands for 2^(e - 127)
+// (255: NaN).
+//
+// One (block, kv head) tile is 16 rows of D / 2 bytes of codes, then 16 rows of D / 32 scale
+// bytes: 17 D / 2 bytes, a multiple of 16.  Within a row, 16-bit word g * (D / 32) + b holds
+// dims 32 b + 4 g .. 32 b + 4 g + 3, the lowest dim in the lowest four bits: four neighbouring
+// words belong to the row's four scale blocks, so that a lane which loads 8 or 16 consecutive
+// bytes of a row holds the same few dims of every block, as an MMA fragment per block needs.
+#pragma once
+
+#include "pa_common.cuh"
+
+namespace pa {
+
+template <int D>
+struct Mx {
+  static constexpr int kBlocks = D / 32;              // scale blocks of a row
+  static constexpr int kRowBytes = D / 2;             // codes of a row
+  static constexpr int kCodeBytes = kBlockSize * kRowBytes;
+  static constexpr int kTileBytes = kCodeBytes + kBlockSize * kBlocks;
+};
+inline int mx_tile_bytes(int head_dim) { return head_dim * 17 / 2; }
+
+// 16-bit word of a row that holds dims d .. d + 3 (d a multiple of 4).
+__host__ __device__ constexpr int mx_word_of(int d, int blocks) {
+  return ((d & 31) >> 2) * blocks + (d >> 5);
+}
+
+// Eight E2M1 codes to four exact f16 pairs, byte i (low nibble in the low half) to out[i].
+__device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t w, uint32_t (&out)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
+      : "r"(w));
+}
+
+// Two fp32 to E2M1, round to nearest even, saturating at 6: `lo` -> low nibble.
+__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+  uint32_t out;
+  asm("{\n\t.reg .b8 t;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
+      "mov.b32 %0, {t, 0, 0, 0};\n\t}"
+      : "=r"(out)
+      : "f"(hi), "f"(lo));
+  return out & 0xffu;
+}
+
+// Scale byte `i` of a word as fp32.  Byte 0 gives 0 instead of 2^-127 (what it scales is below
+// fp32's normal range), and byte 255 gives infinity: the codes of a NaN block are zeros, so their
+// product with it is NaN.
+__device__ __forceinline__ float e8m0_to_f32(uint32_t word, int i) {
+  return __uint_as_float(i == 3 ? (word >> 1) & 0x7f800000u : (word << (23 - 8 * i)) & 0x7f800000u);
+}
+
+// Transposes the 8 x 8 matrix of 16-bit elements that the warp holds two to a lane.
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// Untiled bulk copy of `bytes` (a multiple of 16) from global to shared memory, both 16-byte
+// aligned, completion counted on an mbarrier.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+}  // namespace pa

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -56,6 +57,7 @@ struct AttnArgs {
   uint64_t* span = nullptr;         // benchmark hook: kernel start / end times (pa.h)
   uint64_t wait_ns = 0;             // limit of every bounded device-side wait
   int32_t skip_copy = 0;            // test hook (pa_test_skip_one_copy)
+  float* lse = nullptr;             // [T][Hq] log2-domain log-sum-exp of every row, or NULL
 };
 
 // Workspace carve-up; a pure function of the step's shape (see workspace_layout).
@@ -76,6 +78,16 @@ WsLayout workspace_layout(int32_t num_seqs, int32_t num_q_tokens, int32_t num_q_
                           int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
                           int32_t max_query_len);
 
+// The attention's workspace followed by what the key weights need.
+struct KeyWeightsLayout {
+  size_t lse;          // float [num_q_tokens][num_q_heads], log2 domain
+  size_t chunk_start;  // int32 [num_seqs + 1], prefix sums of the sequences' key chunks
+  size_t total;
+};
+KeyWeightsLayout key_weights_layout(int32_t num_seqs, int32_t num_q_tokens, int32_t num_q_heads,
+                                    int32_t num_kv_heads, int32_t head_dim,
+                                    int32_t max_context_len, int32_t max_query_len);
+
 cudaError_t launch_cache_append(const void* k, const void* v, const int64_t* slots,
                                 int32_t num_tokens, void* k_cache, void* v_cache,
                                 const pa_cache_desc& c, uint32_t* err, cudaStream_t stream);
@@ -91,6 +103,29 @@ pa_status check_attention_args(const void* q, int32_t num_q_tokens, const void* 
                                int32_t num_seqs, int32_t max_context_len, int32_t max_query_len,
                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                float scale, const void* out, int32_t out_dtype, bool* nothing);
+
+cudaError_t launch_cache_read(const int64_t* slots, int32_t num_tokens, const void* k_cache,
+                              const void* v_cache, const pa_cache_desc& c, void* k_out,
+                              void* v_out, bool out_bf16, uint32_t* err, cudaStream_t stream);
+
+// Arguments of the eviction kernels (evict.cu).
+struct EvictArgs {
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  const int32_t* block_tables;
+  const int32_t* dst_tables;
+  const int32_t* context_lens;
+  const int32_t* keep_lens;
+  float* key_weights;       // [num_weight_rows][Hkv][max_keys]
+  const int32_t* weight_rows;
+  const int32_t* dst_weight_rows;
+  int32_t* kept;            // [S][Hkv][max_keep_len]
+  int32_t* new_lens;        // [S]
+  uint32_t* err;
+  int32_t num_seqs, num_blocks, num_kv_heads, head_dim, cache_dtype, max_blocks_per_seq;
+  int32_t max_context_len, max_keep_len, recent, num_weight_rows, max_keys;
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 
 cudaError_t launch_wait_timeout_selftest(uint32_t* err, uint64_t limit_ns, cudaStream_t stream);
 
@@ -131,6 +166,31 @@ struct PoolMaps;
 cudaError_t launch_attention(const AttnArgs& a, const WsLayout& ws, const PoolMaps& maps,
                              bool prefill, cudaEvent_t before, cudaEvent_t after);
 
+// Arguments of the key-weight kernels (key_weights.cu): the step's, the rows' log-sum-exps and
+// the weights.
+struct KeyWeightsArgs {
+  const __nv_bfloat16* q;
+  const uint8_t* k_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* qsl;
+  const float* lse;         // [T][Hq], log2 domain
+  const int32_t* weight_rows;
+  float* key_weights;       // [num_weight_rows][Hkv][max_keys]
+  int32_t* chunk_start;     // [S + 1] scratch
+  uint32_t* err;
+  int32_t num_seqs, num_blocks, max_blocks_per_seq, max_context_len, max_query_len;
+  int32_t num_q_heads, num_kv_heads, head_dim, cache_dtype;
+  int32_t num_weight_rows, max_keys;
+  float score_log2, decay;
+};
+cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t stream);
+
+struct DecodeParams;
+// MXFP4 pools (decode_mx.cu): row tiles of 8 rows of an item, and the attention kernel.
+int mx_row_tiles(int32_t max_query_len, int32_t group);
+cudaError_t launch_decode_mx(const AttnArgs& a, int pmax, const DecodeParams& p);
+
 struct WsHeader;
 
 // Parameters of the tensor-core prefill kernels (prefill.cu, chunk.cu).
@@ -157,6 +217,7 @@ struct PrefillParams {
   float* part_lse;       // [T][Hq][pmax] log2-domain log-sum-exp of split partials
   float* part_o;         // [T][Hq][pmax][128] normalised split partials
   int32_t pmax;          // partials per row the workspace holds (>= the splits of a pair)
+  float* lse;            // [T][Hq] log2-domain log-sum-exp of rows that are not split, or NULL
 };
 
 // Where split prefill tiles keep their partials (the workspace's split-KV arrays).

@@ -831,6 +831,9 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
           p.part_lse[(static_cast<int64_t>(I.t0 + tok) * p.num_q_heads + I.h * G + r % G) *
                          p.pmax + I.k] =
               (seen && l > 0.f) ? m_used + __log2f(l) - (kFp8 ? 8.f : 0.f) : -CUDART_INF_F;
+        if (p.lse && !split && half == 0 && row_ok)
+          p.lse[static_cast<int64_t>(I.t0 + tok) * p.num_q_heads + I.h * G + r % G] =
+              l == 0.f ? -CUDART_INF_F : m_used + __log2f(l) - (kFp8 ? 8.f : 0.f);
         if (!bf16) {
           constexpr int CH = kOC / 4;   // 16-byte chunks of the thread's row part
 #pragma unroll
@@ -962,6 +965,7 @@ cudaError_t launch_prefill(const AttnArgs& a, const int32_t* item_start, const i
   p.wait_ns = a.wait_ns;
   p.skip_copy = a.skip_copy;
   p.span = a.span ? a.span + 2 : nullptr;
+  p.lse = a.lse;
   p.part_lse = scratch.part_lse;
   p.part_o = scratch.part_o;
   p.pmax = scratch.pmax;
