@@ -237,6 +237,17 @@ KeyWeightsLayout key_weights_layout(int32_t S, int32_t T, int32_t Hq, int32_t Hk
   size_t off = up(workspace_layout(S, T, Hq, Hkv, D, max_ctx, max_q).total);
   w.lse = off;
   off = up(off + sizeof(float) * size_t(std::max(T, 0)) * size_t(std::max(Hq, 0)));
+  // Scores of the runs of at most 16 rows (decode tokens, short verify runs), which the finishing
+  // kernel reads instead of K: 8 bytes per row and key against K's bytes per key.  Not beyond 1 GiB
+  // (they are bounded by the longest context, not by the keys there are): K is read again then.
+  const int64_t G = Hkv > 0 ? Hq / Hkv : 1;
+  w.score_rows = static_cast<int32_t>(std::min<int64_t>(kDecodeMaxRows, std::max(max_q, 1) * G));
+  w.score_stride = (std::max(max_ctx, 1) + kBlockSize - 1) / kBlockSize * kBlockSize;
+  const double bytes = 4.0 * std::max(S, 0) * std::max(Hkv, 0) * w.score_rows * w.score_stride;
+  if (bytes > double(1 << 30)) w.score_rows = 0;
+  w.scores = off;
+  off = up(off + sizeof(float) * size_t(std::max(S, 0)) * size_t(std::max(Hkv, 0)) *
+                     size_t(w.score_rows) * size_t(w.score_stride));
   w.chunk_start = off;
   off = up(off + sizeof(int32_t) * (size_t(std::max(S, 0)) + 1));
   w.total = off;
@@ -429,6 +440,11 @@ size_t pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_tokens, int32
       .total;
 }
 
+struct Scores {  // where the split-KV path writes its scores (DecodeParams)
+  float* data = nullptr;
+  int32_t rows = 0, stride = 0;
+};
+
 // Attention of one step; `lse` ([num_q_tokens][num_q_heads], or NULL) also receives the rows'
 // log-sum-exps in the log2 domain.
 static pa_status attend(const void* q, int32_t num_q_tokens, const void* k_cache,
@@ -438,7 +454,7 @@ static pa_status attend(const void* q, int32_t num_q_tokens, const void* k_cache
                         int32_t num_seqs, int32_t max_context_len, int32_t max_query_len,
                         int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
                         void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes,
-                        cudaStream_t stream, float* lse) {
+                        cudaStream_t stream, float* lse, const Scores& scores) {
   bool nothing = false;
   pa_status st = pa::check_attention_args(
       q, num_q_tokens, k_cache, v_cache, cache, block_tables, max_blocks_per_seq, context_lens,
@@ -489,6 +505,9 @@ static pa_status attend(const void* q, int32_t num_q_tokens, const void* k_cache
   a.skip_copy = g_skip_copy;
   a.span = g_span;
   a.lse = lse;
+  a.scores = scores.data;
+  a.score_rows = scores.rows;
+  a.score_stride = scores.stride;
   cudaError_t e = pa::launch_attention(a, ws, maps, use_prefill, g_before, g_after);
   if (e != cudaSuccess) return cuda_fail(e, "pa_attention launch");
   return PA_OK;
@@ -506,7 +525,7 @@ pa_status pa_attention(const void* q, int32_t num_q_tokens, const void* k_cache,
   return attend(q, num_q_tokens, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
                 context_lens, query_start_loc, num_seqs, max_context_len, max_query_len,
                 num_q_heads, num_kv_heads, head_dim, scale, out, out_dtype, workspace,
-                workspace_bytes, stream, nullptr);
+                workspace_bytes, stream, nullptr, Scores{});
 }
 
 size_t pa_attention_key_weights_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
@@ -548,10 +567,12 @@ pa_status pa_attention_key_weights(
                 ws.total);
   uint8_t* wsb = static_cast<uint8_t*>(workspace);
   float* lse = reinterpret_cast<float*>(wsb + ws.lse);
+  const Scores scores{ws.score_rows ? reinterpret_cast<float*>(wsb + ws.scores) : nullptr,
+                      ws.score_rows, ws.score_stride};
   st = attend(q, num_q_tokens, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
               context_lens, query_start_loc, num_seqs, max_context_len, max_query_len, num_q_heads,
               num_kv_heads, head_dim, scale, out, out_dtype, workspace, workspace_bytes, stream,
-              lse);
+              lse, scores);
   if (st != PA_OK) return st;
   pa::KeyWeightsArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(q);
@@ -562,6 +583,10 @@ pa_status pa_attention_key_weights(
   a.lse = lse;
   a.weight_rows = weight_rows;
   a.key_weights = key_weights;
+  a.scores = scores.data;
+  a.score_rows = ws.score_rows;
+  a.score_stride = ws.score_stride;
+  a.k_pass = int64_t(max_query_len) * (num_q_heads / num_kv_heads) > ws.score_rows;
   a.chunk_start = reinterpret_cast<int32_t*>(wsb + ws.chunk_start);
   a.err = static_cast<uint32_t*>(workspace);
   a.num_seqs = num_seqs;

@@ -348,7 +348,8 @@ constexpr int decode_smem_bytes() {
 // Instances with 2-stage rings are held to 3 CTAs per SM (at most 170 registers a thread): the
 // kernel is latency-bound per SM, and the third CTA's warps, which the smaller rings leave room
 // for in shared memory, keep more blocks in flight.
-template <int D, bool kFp8, int NST, int RT, int HPI>
+// kScores: every score is also written out, for the key weights (key_weights.cu).
+template <int D, bool kFp8, int NST, int RT, int HPI, bool kScores>
 __global__ void __launch_bounds__(kDecodeWarps * 32, NST == 2 ? 3 : 1)
     decode_kernel(const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const DecodeParams p) {
@@ -417,6 +418,19 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, NST == 2 ? 3 : 1)
       row_pos[r] = I.pos_base + row_tok[r];
     }
     const int my_head = HPI > 1 ? quad / p.group : 0;  // head of the item this lane's row uses
+    float* score_row[RT];  // where this lane's rows' scores go, or NULL
+    if constexpr (kScores) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        // rows of earlier tiles of the run, then the head's rows in this one
+        const int row = I.qt * (R / (p.group * HPI)) * p.group + quad + 8 * r - my_head * p.group;
+        score_row[r] =
+            row_ok[r] && I.run * p.group <= p.score_rows
+                ? p.scores + ((static_cast<int64_t>(I.s) * p.num_kv_heads + I.h + my_head) *
+                                  p.score_rows + row) * p.score_stride
+                : nullptr;
+      }
+    }
     const int pos_last = I.pos_base + I.n - 1;
 
     // ---- table entries of this warp's blocks, one per lane -----------------------------
@@ -612,6 +626,14 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, NST == 2 ? 3 : 1)
               const bool ok = row_ok[r] && kidx <= row_pos[r];
               sv[2 * nt + e] = ok ? sacc[nt][2 * r + e] * row_scale[r] : -CUDART_INF_F;
             }
+          if constexpr (kScores) {
+            if (score_row[r]) {
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt)
+                *reinterpret_cast<float2*>(score_row[r] + key0 + 8 * nt + 2 * qc) =
+                    make_float2(sv[2 * nt], sv[2 * nt + 1]);
+            }
+          }
           float mloc = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
           mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 1));
           mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 2));
@@ -954,12 +976,16 @@ static cudaError_t run_merge(const AttnArgs& a, const DecodeParams& p) {
   return e;
 }
 
-template <int D, bool kFp8, int NST, int RT, int HPI = 1>
+template <int D, bool kFp8, int NST, int RT, int HPI = 1, bool kScores = false>
 static cudaError_t run_decode(const AttnArgs& a, const WsLayout& ws, const DecodeParams& p,
                               const CUtensorMap& kmap, const CUtensorMap& vmap,
                               cudaEvent_t before, cudaEvent_t after) {
+  if constexpr (!kScores) {
+    if (p.scores)
+      return run_decode<D, kFp8, NST, RT, HPI, true>(a, ws, p, kmap, vmap, before, after);
+  }
   constexpr int smem = decode_smem_bytes<D, kFp8, NST, HPI>();
-  auto kern = decode_kernel<D, kFp8, NST, RT, HPI>;
+  auto kern = decode_kernel<D, kFp8, NST, RT, HPI, kScores>;
   LaunchInfo li;
   cudaError_t e = launch_info(kern, kDecodeWarps * 32, smem, &li);
   if (e != cudaSuccess) return e;
@@ -1054,6 +1080,9 @@ cudaError_t launch_attention(const AttnArgs& a, const WsLayout& ws, const PoolMa
   const bool rt2 = p.group > 8 || (!mixed && static_cast<int64_t>(dec_q) * p.group > 8);
   p.rows_per_tile = mx ? 8 * mx_row_tiles(a.max_query_len, p.group) : rt2 ? 16 : 8;
   p.lse = a.lse;
+  p.scores = a.scores;
+  p.score_rows = a.score_rows;
+  p.score_stride = a.score_stride;
 
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

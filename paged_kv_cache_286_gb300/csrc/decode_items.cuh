@@ -44,6 +44,10 @@ struct DecodeParams {
   uint64_t wait_ns;        // limit of every bounded wait
   int32_t skip_copy;       // test hook: item 0 leaves out its first tile copy (see pa.h)
   float* lse;              // [T][Hq] log2-domain log-sum-exp of every row, or NULL
+  float* scores;           // [S][Hkv][score_rows][score_stride] log2-domain scores of the runs of
+                           // up to score_rows rows (row = token x group + head), or NULL
+  int32_t score_rows;
+  int32_t score_stride;
 };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -73,7 +77,7 @@ __device__ __forceinline__ int decode_items_of(const DecodeParams& p, int n, int
 }
 
 struct ItemInfo {
-  int s, h, qt, part, t0, n, L, nparts, blk_begin, blk_end, pos_base, rows, valid, idx;
+  int s, h, qt, part, t0, n, L, nparts, blk_begin, blk_end, pos_base, rows, valid, idx, run;
 };
 
 // Claims the next item from the step's counter: R rows per tile, HPI kv heads per item.
@@ -113,6 +117,7 @@ __device__ __forceinline__ ItemInfo claim_item(const DecodeParams& p, int total_
     info.blk_end = min((part + 1) * p.pblk, blk_tile);
     info.pos_base = L - n + tok_begin;                 // position of the tile's first token
     info.rows = info.n * p.group * HPI;
+    info.run = n;                                      // query tokens of the whole run
   }
   return info;
 }

@@ -46,7 +46,9 @@ struct MxCfg {
   static_assert(kStageBytes % 16 == 0 && sizeof(ItemInfo) <= 64, "");
 };
 
-template <int D, int RT>
+// kScores: the scores of runs of up to kDecodeMaxRows rows are also written out, for the key
+// weights (key_weights.cu).
+template <int D, int RT, bool kScores>
 __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
     decode_mx_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool,
                      const DecodeParams p) {
@@ -268,6 +270,17 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
             s[rt][i] *= row_scale[rt][i & 1];
             if (diag && key0 + my_key + 8 * (i >> 1) > row_pos[rt][i & 1]) s[rt][i] = -CUDART_INF_F;
           }
+          if constexpr (kScores) {
+            if (I.run * p.group <= p.score_rows) {  // one tile then: its rows are the run's
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int row = 8 * rt + 2 * qc + (i & 1);
+                if (row < I.rows)
+                  p.scores[((static_cast<int64_t>(I.s) * p.num_kv_heads + I.h) * p.score_rows + row) *
+                               p.score_stride + key0 + my_key + 8 * (i >> 1)] = s[rt][i];
+              }
+            }
+          }
           const bool over = s[rt][0] > m_run[rt][0] + kLazyRescaleLog2 ||
                             s[rt][2] > m_run[rt][0] + kLazyRescaleLog2 ||
                             s[rt][1] > m_run[rt][1] + kLazyRescaleLog2 ||
@@ -477,9 +490,12 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
               static_cast<unsigned long long>(global_ns()));
 }
 
-template <int D, int RT>
+template <int D, int RT, bool kScores = false>
 static cudaError_t run_mx(const AttnArgs& a, int pmax, const DecodeParams& p) {
-  auto kern = decode_mx_kernel<D, RT>;
+  if constexpr (!kScores) {
+    if (p.scores) return run_mx<D, RT, true>(a, pmax, p);
+  }
+  auto kern = decode_mx_kernel<D, RT, kScores>;
   constexpr int smem = MxCfg<D, RT>::kSmem;
   LaunchInfo li;
   cudaError_t e = launch_info(kern, kDecodeWarps * 32, smem, &li);

@@ -32,20 +32,80 @@ constexpr int kKwRows = 64;             // rows staged in shared memory at a tim
 
 enum class Pool { kBf16, kE4m3, kMx };
 
-// Items of a sequence: its key chunks (for each kv head), none when it does not accumulate.
-__device__ __forceinline__ int kw_chunks(const KeyWeightsArgs& a, int s, uint32_t* err_bits) {
+// Whether a sequence accumulates weights in this step.
+__device__ __forceinline__ bool kw_accumulates(const KeyWeightsArgs& a, int s,
+                                               uint32_t* err_bits) {
   const int n = a.qsl[s + 1] - a.qsl[s], L = a.context_lens[s];
   // (what the attention's plan flags and skips is skipped here too)
   if (n <= 0 || n > L || L > a.max_context_len || n > a.max_query_len ||
       L > a.max_blocks_per_seq * kBlockSize)
-    return 0;
+    return false;
   const int row = a.weight_rows ? a.weight_rows[s] : s;
-  if (row < 0) return 0;
+  if (row < 0) return false;
   if (row >= a.num_weight_rows) {
     *err_bits |= PA_DEVERR_WEIGHT_ROW;
-    return 0;
+    return false;
   }
-  return (L + kKwKeys - 1) / kKwKeys;
+  return true;
+}
+
+// Items of a sequence for the kernel that reads K: its key chunks, if its scores were not kept.
+__device__ __forceinline__ int kw_chunks(const KeyWeightsArgs& a, int s, uint32_t* err_bits) {
+  if (!kw_accumulates(a, s, err_bits)) return 0;
+  if ((a.qsl[s + 1] - a.qsl[s]) * (a.num_q_heads / a.num_kv_heads) <= a.score_rows) return 0;
+  return (a.context_lens[s] + kKwKeys - 1) / kKwKeys;
+}
+
+// Runs whose scores the attention kept: one CTA per (sequence, kv head) and equal share of its
+// keys, four neighbouring keys (of one block) to a thread.  Bound by the scores' bytes (mostly
+// L2's) and by launch.
+constexpr int kFinThreads = 256;
+constexpr int kFinShare = 2048;  // keys of a share at least (of the longest sequence)
+__global__ void __launch_bounds__(kFinThreads) kw_finish_kernel(const KeyWeightsArgs a) {
+  __shared__ float s_lse[kDecodeMaxRows];
+  grid_dependency_wait();
+  const int s = blockIdx.x / a.num_kv_heads, h = blockIdx.x - s * a.num_kv_heads;
+  uint32_t bits = 0;
+  const bool ok = kw_accumulates(a, s, &bits);
+  if (bits && threadIdx.x == 0) set_error(a.err, bits);
+  if (!ok) return;
+  const int t0 = a.qsl[s], n = a.qsl[s + 1] - t0, L = a.context_lens[s];
+  const int G = a.num_q_heads / a.num_kv_heads;
+  if (n * G > a.score_rows) return;
+  if (threadIdx.x < n * G)
+    s_lse[threadIdx.x] = a.lse[static_cast<int64_t>(t0 + threadIdx.x / G) * a.num_q_heads + h * G +
+                               threadIdx.x % G];
+  __syncthreads();
+  const int row = a.weight_rows ? a.weight_rows[s] : s;
+  float* W = a.key_weights + (static_cast<int64_t>(row) * a.num_kv_heads + h) * a.max_keys;
+  const float* sc = a.scores + (static_cast<int64_t>(s) * a.num_kv_heads + h) * a.score_rows *
+                                   a.score_stride;
+  const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
+  const int groups = (L + 3) / 4;
+  const int share = (groups + gridDim.y - 1) / gridDim.y;
+  const int end = min(groups, share * (static_cast<int>(blockIdx.y) + 1));
+  for (int g = share * blockIdx.y + threadIdx.x; g < end; g += kFinThreads) {
+    const int key = 4 * g;
+    float w[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = key + i < L ? W[key + i] : 0.f;
+    const int phys = __ldg(table + key / kBlockSize);
+    if (phys >= 0 && phys < a.num_blocks) {  // (the attention leaves bad blocks out)
+      const float* col = sc + key;
+#pragma unroll 4
+      for (int r = 0; r < n * G; ++r) {
+        const float4 x = *reinterpret_cast<const float4*>(col + static_cast<int64_t>(r) * a.score_stride);
+        const int pos = L - n + r / G;  // the row's position: it sees keys up to this one
+        const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (key + i <= pos) sum[i] += fast_exp2(v[i] - s_lse[r]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (key + i < L) W[key + i] = fmaf(a.decay, w[i], sum[i]);
+  }
 }
 
 // One CTA: exclusive prefix sums of the sequences' chunks.
@@ -257,7 +317,17 @@ cudaError_t run_key_weights(const KeyWeightsArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t stream) {
-  cudaError_t e = launch_dependent(kw_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
+  cudaError_t e = cudaSuccess;
+  if (a.scores) {
+    const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+    const int64_t shares = std::min<int64_t>((a.max_context_len + int64_t(kFinShare) - 1) / kFinShare, 64);
+    if (pairs > INT32_MAX) return cudaErrorInvalidValue;
+    e = launch_dependent(kw_finish_kernel, dim3(static_cast<unsigned>(pairs), unsigned(shares)),
+                         dim3(kFinThreads), 0, stream, a);
+    if (e != cudaSuccess) return e;
+  }
+  if (!a.k_pass) return cudaSuccess;
+  e = launch_dependent(kw_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
   if (e != cudaSuccess) return e;
   if (a.cache_dtype == PA_FP8_E4M3) return run_key_weights<Pool::kE4m3, 128>(a, stream);
   if (a.cache_dtype == PA_MXFP4)

@@ -58,6 +58,9 @@ struct AttnArgs {
   uint64_t wait_ns = 0;             // limit of every bounded device-side wait
   int32_t skip_copy = 0;            // test hook (pa_test_skip_one_copy)
   float* lse = nullptr;             // [T][Hq] log2-domain log-sum-exp of every row, or NULL
+  float* scores = nullptr;          // scores of the split-KV path's rows, or NULL (DecodeParams)
+  int32_t score_rows = 0;
+  int32_t score_stride = 0;
 };
 
 // Workspace carve-up; a pure function of the step's shape (see workspace_layout).
@@ -81,6 +84,9 @@ WsLayout workspace_layout(int32_t num_seqs, int32_t num_q_tokens, int32_t num_q_
 // The attention's workspace followed by what the key weights need.
 struct KeyWeightsLayout {
   size_t lse;          // float [num_q_tokens][num_q_heads], log2 domain
+  size_t scores;       // float [num_seqs][num_kv_heads][score_rows][score_stride]
+  int32_t score_rows;  // 0: none are kept
+  int32_t score_stride;
   size_t chunk_start;  // int32 [num_seqs + 1], prefix sums of the sequences' key chunks
   size_t total;
 };
@@ -175,6 +181,9 @@ struct KeyWeightsArgs {
   const int32_t* context_lens;
   const int32_t* qsl;
   const float* lse;         // [T][Hq], log2 domain
+  const float* scores;      // of the runs of up to score_rows rows (DecodeParams), or NULL
+  int32_t score_rows, score_stride;
+  int32_t k_pass;           // some run may have more rows than that: the kernel that reads K runs
   const int32_t* weight_rows;
   float* key_weights;       // [num_weight_rows][Hkv][max_keys]
   int32_t* chunk_start;     // [S + 1] scratch

@@ -360,6 +360,23 @@ def test_key_weights(kind, d, qlens, ctx, hq, hkv):
     assert torch.equal(W, W2)
 
 
+def test_key_weights_of_a_step_whose_scores_are_not_kept():
+    """A bound on the context so large that the scores would take more than 1 GiB: K is read again."""
+    import paged_kv_cache_286_gb300 as pa
+    c = Case([300, 70, 1000], [1, 2, 1], 8, 2, 128, "bf16", seed=5)
+    t, ctx, qsl = c.dev()
+    far = 12_000_000
+    sizes = [pa.attention_key_weights_workspace_size(3, 4, 8, 2, 128, m, 2) for m in (far - 8_000_000, far)]
+    assert sizes[1] < sizes[0] + (1 << 29)
+    W = torch.zeros(3, 2, far, device="cuda")
+    ws = pa.new_workspace(sizes[1])
+    hints = dict(c.hints(), max_context_len=far)
+    pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, ctx, qsl, W, ws, **hints)
+    assert pa.check_error(ws) == 0
+    W = W[..., :1003].contiguous()
+    check_weights(c, np.zeros(W.shape, np.float32), W.cpu().numpy(), [0, 1, 2], 1.0)
+
+
 def test_key_weights_rows_left_out():
     import paged_kv_cache_286_gb300 as pa
     c = Case([40, 70, 33], [1, 2, 1], 4, 2, 64, "bf16", seed=2)
