@@ -334,7 +334,8 @@ void pa_set_wait_limit_ns(uint64_t ns);
  * launches (the first copy of the first work item claimed) while that copy's barrier still
  * expects the bytes, so that the bounded waits on it expire and the call ends with
  * PA_ERR_TIMEOUT without any fault: the expiry and drain paths of the kernels can be exercised
- * on a real GPU. */
+ * on a real GPU.  (The split-KV kernel of MXFP4 pools has no wait that could run out and ignores
+ * the hook.) */
 void pa_test_skip_one_copy(int32_t enable);
 
 /* Self-test of the bounded wait: one thread waits, for limit_ns (in (0, 10 s]), on an mbarrier

@@ -6,8 +6,11 @@
 //  * Work items, plan and merge are those of the split-KV kernel (decode.cu): an item is
 //    (sequence, kv head, tile of 8 RT rows = tokens x heads of the group, KV partition), each of
 //    the CTA's 4 warps takes every 4th block of the partition through its own ring of shared
-//    memory stages.  A (block, head) tile is contiguous, so one untiled bulk copy each brings the
-//    K and the V tile.
+//    memory stages, filled by 16-byte asynchronous copies of the whole warp: a tile is 68 of them
+//    and contiguous, so it takes three instructions, and their completion one more, where an
+//    elected lane's bulk copies with an mbarrier take some 60 issue slots a block.  (The codes are
+//    a quarter of bf16's bytes: issue slots, not bytes in flight, are what this kernel runs out
+//    of.)
 //  * The MMAs (m16n8k16, f16) have the keys (S^T = K q^T) and the head dims (O^T = V^T P^T) as M:
 //    a block's 16 keys fill M where the rows would leave half of it empty, codes are converted
 //    to f16 (exact) once for all row tiles, and S^T's accumulators become P^T's B operand by one
@@ -25,6 +28,8 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <cfloat>
+#include <type_traits>
 
 #include "decode_items.cuh"
 #include "mxfp4.cuh"
@@ -35,14 +40,14 @@ namespace pa {
 
 template <int D, int RT>
 struct MxCfg {
-  static constexpr int kStages = RT == 1 ? 6 : 8;
+  static constexpr int kStages = 4;
   static constexpr int kStageBytes = 2 * Mx<D>::kTileBytes;
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kScratch = 8 * RT * D * 4 + 2 * 8 * RT * 4;  // O, max and sum of a warp
-  static constexpr int kSmem =
-      kDecodeWarps * kWarpBytes + kDecodeWarps * kStages * 8 + 2 * 64 + 128 /*alignment*/;
+  static constexpr int kQBytes = RT * Mx<D>::kBlocks * 512;  // q fragments of an item
+  static constexpr int kSmem = kDecodeWarps * (kWarpBytes + kScratch) + 2 * kQBytes +
+                               2 * 8 * RT * 4 /*row scales*/ + 3 * 64 /*items*/ + 128 /*alignment*/;
   static constexpr int kCtas = RT == 1 ? 4 : RT == 2 ? 3 : 2;  // CTAs per SM
-  static_assert(kScratch <= kWarpBytes, "merge scratch must fit in a warp's stages");
   static_assert(kStageBytes % 16 == 0 && sizeof(ItemInfo) <= 64, "");
 };
 
@@ -60,153 +65,179 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDecodeWarps * C::kWarpBytes);
-  ItemInfo* s_item = reinterpret_cast<ItemInfo*>(bars + kDecodeWarps * NST);
+  float* scratch = reinterpret_cast<float*>(smem + kDecodeWarps * C::kWarpBytes);  // [warp]
+  uint4* s_q = reinterpret_cast<uint4*>(smem + kDecodeWarps * (C::kWarpBytes + C::kScratch));
+  float* s_scale = reinterpret_cast<float*>(s_q + 2 * C::kQBytes / 16);
+  ItemInfo* s_item = reinterpret_cast<ItemInfo*>(s_scale + 2 * R);
 
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   const int quad = lane >> 2;
   const int qc = lane & 3;
   uint8_t* wbuf = smem + warp * C::kWarpBytes;
-  uint64_t* wbars = bars + warp * NST;
   // Key of the block that row `quad` of the MMA's upper half stands for (quad + 8: that key + 8).
-  // P^T's k indices 2 qc, 2 qc + 1 then are keys qc and 4 + (qc ^ 1): the 64-byte rows that the
-  // lanes of one shared memory access touch have both parities for K's 16-byte and for V's
-  // 8-byte loads (natural order: V's conflict four ways).
+  // P^T's k indices 2 qc, 2 qc + 1 then are keys qc and 4 + (qc ^ 1), so that the lanes of one
+  // shared memory access touch rows of both parities for K's 16-byte and for V's 8-byte loads
+  // (natural order: V's conflict four ways).  With 64-byte rows, the 32-byte halves of V's rows
+  // with bit 1 set are swapped on the way in, which makes V's loads free of conflicts.
   const int my_key = (quad & 1) ? 4 + ((quad >> 1) ^ 1) : quad >> 1;
 
-  if (lane == 0) {
-    for (int st = 0; st < NST; ++st) mbar_init(&wbars[st], 1);
-    fence_barrier_init();
-  }
-  __syncthreads();
   grid_dependency_wait();
   if (p.span && threadIdx.x == 0)
     atomicMin(reinterpret_cast<unsigned long long*>(p.span),
               static_cast<unsigned long long>(global_ns()));
   const int total_items = p.item_start[p.num_seqs];
-  uint32_t it = 0;
-  bool timed_out = false;
-  auto fetch_item = [&](ItemInfo* dst) { *dst = claim_item<R, 1>(p, total_items); };
-  if (threadIdx.x == 0) fetch_item(&s_item[0]);
-  int cur = 0;
+  // this lane's 16-byte pieces of a tile: `lane`, 32 + lane, ... ; where they land (V: swapped)
+  constexpr int kPieces = M::kTileBytes / 16;
+  constexpr int kFull = kPieces / 32, kTail = kPieces % 32;
+  const bool tail = lane < kTail;
+  const uint32_t kdst = smem_u32(wbuf) + lane * 16;
+  const uint32_t vdst = smem_u32(wbuf) + M::kTileBytes +
+                        (NB == 4 ? lane ^ ((lane >> 3 & 1) << 1) : lane) * 16;
+  const uint32_t vdst_tail = smem_u32(wbuf) + M::kTileBytes + (32 * kFull + lane) * 16;
 
-  while (true) {
-    const bool any_timeout = __syncthreads_or(timed_out) != 0;
-    const ItemInfo I = s_item[cur];
-    if (!I.valid || any_timeout) break;
-    const uint32_t it0 = it;
-    const int pos_last = I.pos_base + I.n - 1;
-
-    // ---- table entries of this warp's blocks, one per lane -----------------------------
-    const int my_first = I.blk_begin + warp;
-    const int nb_w = my_first < I.blk_end ? ceil_div(I.blk_end - my_first, kDecodeWarps) : 0;
-    int phys_lane = -1;
-    if (lane < nb_w) {
-      const int b = my_first + lane * kDecodeWarps;
-      phys_lane = __ldg(p.block_tables + static_cast<int64_t>(I.s) * p.max_blocks_per_seq + b);
-      if (phys_lane < 0 || phys_lane >= p.num_blocks) {
-        set_error(&p.hdr->error, PA_DEVERR_BLOCK_ID);
-        phys_lane = -1;
+  // Items follow one another without a pause of the copies: while an item runs, thread 0 claims
+  // the one after the next, the next one's table entries and q fragments are brought in, and the
+  // copies run on into its blocks.
+  auto blocks_of = [&](const ItemInfo& I) {  // blocks of the item that are this warp's
+    const int first = I.blk_begin + warp;
+    return I.valid && first < I.blk_end ? ceil_div(I.blk_end - first, kDecodeWarps) : 0;
+  };
+  // (block, kv head) tile of this lane's block of the item, or -1
+  auto tile_of = [&](const ItemInfo& I, int nb) {
+    if (lane >= nb) return -1;
+    const int b = I.blk_begin + warp + lane * kDecodeWarps;
+    const int phys = __ldg(p.block_tables + static_cast<int64_t>(I.s) * p.max_blocks_per_seq + b);
+    if (phys < 0 || phys >= p.num_blocks) {
+      set_error(&p.hdr->error, PA_DEVERR_BLOCK_ID);
+      return -1;
+    }
+    return phys * p.num_kv_heads + I.h;  // (the pool has fewer than 2^31 rows)
+  };
+  // copies of one block (tile < 0: none) into stage `to`, one group whatever is copied
+  auto issue = [&](int tile, int to) {
+    if (tile >= 0) {
+      const int64_t at = static_cast<int64_t>(tile) * M::kTileBytes + lane * 16;
+      const uint32_t so = to * C::kStageBytes;
+#pragma unroll
+      for (int i = 0; i < kFull; ++i) {
+        cp_async16(kdst + so + 512 * i, k_pool + at + 512 * i);
+        cp_async16(vdst + so + 512 * i, v_pool + at + 512 * i);
+      }
+      if (tail) {
+        cp_async16(kdst + so + 512 * kFull, k_pool + at + 512 * kFull);
+        cp_async16(vdst_tail + so, v_pool + at + 512 * kFull);
       }
     }
-    auto issue = [&](int k) {  // stage load for the warp's k-th block (all lanes call)
-      const int phys = __shfl_sync(0xffffffffu, phys_lane, k);
-      if (lane == 0) {
-        const uint32_t st = (it0 + k) % NST;
-        uint64_t* bar = &wbars[st];
-        if (phys >= 0) {
-          uint8_t* kt = wbuf + st * C::kStageBytes;
-          const int64_t tile = static_cast<int64_t>(phys) * p.num_kv_heads + I.h;
-          mbar_arrive_expect_tx(bar, C::kStageBytes);
-          // test hook: the first stage of the first item claimed expects its bytes but gets no
-          // copy, so that the bounded wait on it expires
-          if (!(p.skip_copy && I.idx == 0 && warp == 0 && k == 0)) {
-            bulk_load(kt, k_pool + tile * M::kTileBytes, M::kTileBytes, bar);
-            bulk_load(kt + M::kTileBytes, v_pool + tile * M::kTileBytes, M::kTileBytes, bar);
-          }
-        } else {
-          mbar_arrive(bar);
-        }
-      }
-    };
-    const int npre = min(NST, nb_w);
-    for (int k = 0; k < npre; ++k) issue(k);
-    if (threadIdx.x == 0) fetch_item(&s_item[cur ^ 1]);  // read after the next loop-top barrier
+    cp_async_commit();
+  };
+  // q fragments (B operand, n = row quad of the tile) of an item, one warp per row tile: of scale
+  // block b, the pairs of dims 32 b + 8 qc + {0 1, 2 3} (first MMA) and {4 5, 6 7} (second), and
+  // the rows' score scales.  They stay in shared memory: in registers they would cost a CTA per SM.
+  static_assert(RT <= kDecodeWarps, "a warp per row tile");
+  auto stage_q = [&](const ItemInfo& I, int buf) {
+    if (warp >= RT) return;
+    const int row = 8 * warp + quad;
+    const bool ok = row < I.rows;
+    const int tok = ok ? row / p.group : 0, g = ok ? row - tok * p.group : 0;
+    const __nv_bfloat16* qrow =
+        p.q + (static_cast<int64_t>(I.t0 + tok) * p.num_q_heads + I.h * p.group + g) * D;
+    uint4 raw[NB];
+    float amax = 0.f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      raw[b] = ok ? __ldg(reinterpret_cast<const uint4*>(qrow + 32 * b + 8 * qc))
+                  : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        amax = fmaxf(amax, fmaxf(fabsf(bf16lo_to_f32(w[i])), fabsf(bf16hi_to_f32(w[i]))));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // power of two e with amax * 2^e < 2^15 (f16 range), exact scaling
+    const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 126;
+    const int e = max(-100, min(100, 15 - ex));
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+      uint32_t f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f[i] = pack_f16x2(bf16lo_to_f32(w[i]) * up, bf16hi_to_f32(w[i]) * up);
+      s_q[((buf * RT + warp) * NB + b) * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
+    }
+    if (qc == 0)
+      s_scale[buf * R + row] = p.score_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  };
 
-    // ---- q fragments (B operand, n = row quad of the tile): of scale block b, the pairs of
-    // dims 32 b + 8 qc + {0 1, 2 3} (first MMA) and {4 5, 6 7} (second) ---------------------
-    uint32_t qf[RT][NB][4];
+  if (threadIdx.x == 0) {
+    s_item[0] = claim_item<R, 1>(p, total_items);
+    s_item[1] = claim_item<R, 1>(p, total_items);
+  }
+  __syncthreads();
+  int nb_w = blocks_of(s_item[0]);
+  int tile_lane = tile_of(s_item[0], nb_w);
+  if (s_item[0].valid) stage_q(s_item[0], 0);
+  for (int k = 0; k < NST - 1; ++k) {
+    const int tile = __shfl_sync(0xffffffffu, tile_lane, k);
+    issue(k < nb_w ? tile : -1, k);
+  }
+  int st = 0;       // stage of the block that comes next
+  int slot = 0;     // item's place in s_item
+  int buf = 0;      // its place in s_q
+
+  while (true) {
+    __syncthreads();  // the item's q, the next item and the scratch are ready
+    const ItemInfo I = s_item[slot];
+    if (!I.valid) break;
+    const int next_slot = slot == 2 ? 0 : slot + 1;
+    int nb_next, tile_next;
+    {
+      const ItemInfo N = s_item[next_slot];
+      nb_next = blocks_of(N);
+      tile_next = tile_of(N, nb_next);
+      if (N.valid) stage_q(N, buf ^ 1);
+    }
+    if (threadIdx.x == 0) s_item[next_slot == 2 ? 0 : next_slot + 1] = claim_item<R, 1>(p, total_items);
+    const int my_first = I.blk_begin + warp;
+    const int pos_last = I.pos_base + I.n - 1;
+    const uint4* q_frag = s_q + buf * RT * NB * 32 + lane;  // [(rt * NB + b) * 32]
+    const uint32_t there = __ballot_sync(0xffffffffu, tile_lane >= 0);
     float row_scale[RT][2];  // of rows 2 qc, 2 qc + 1 of each tile
     int row_pos[RT][2];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int row = 8 * rt + quad;
-      const bool ok = row < I.rows;
-      const int tok = ok ? row / p.group : 0, g = ok ? row - tok * p.group : 0;
-      const __nv_bfloat16* qrow =
-          p.q + (static_cast<int64_t>(I.t0 + tok) * p.num_q_heads + I.h * p.group + g) * D;
-      uint4 raw[NB];
-      float amax = 0.f;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        raw[b] = ok ? __ldg(reinterpret_cast<const uint4*>(qrow + 32 * b + 8 * qc))
-                    : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          amax = fmaxf(amax, fmaxf(fabsf(bf16lo_to_f32(w[i])), fabsf(bf16hi_to_f32(w[i]))));
-      }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      int ex = 0;  // power of two e with amax * 2^e < 2^15 (f16 range), exact scaling
-      if (amax > 0.f && amax < CUDART_INF_F) frexpf(amax, &ex);
-      const int e = max(-100, min(100, 15 - ex));
-      const float up = ldexpf(1.f, e);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          qf[rt][b][i] = pack_f16x2(bf16lo_to_f32(w[i]) * up, bf16hi_to_f32(w[i]) * up);
-      }
-      const float rs = p.score_log2 * ldexpf(1.f, -e);
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        row_scale[rt][j] = __shfl_sync(0xffffffffu, rs, 4 * (2 * qc + j));
+        row_scale[rt][j] = s_scale[buf * R + 8 * rt + 2 * qc + j];
         row_pos[rt][j] = I.pos_base + (8 * rt + 2 * qc + j) / p.group;
       }
-    }
 
     float m_run[RT][2], l_run[RT][2];  // base (log2 domain) and this lane's share of the sum
     float oacc[RT][2 * NB][4];         // [row tile][2 b + t]: dims 32 b + 4 quad + 2 t + {0, 1}
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      m_run[rt][0] = m_run[rt][1] = -CUDART_INF_F;
+      m_run[rt][0] = m_run[rt][1] = -FLT_MAX;  // any score but -infinity exceeds it
       l_run[rt][0] = l_run[rt][1] = 0.f;
 #pragma unroll
       for (int j = 0; j < 2 * NB; ++j)
         oacc[rt][j][0] = oacc[rt][j][1] = oacc[rt][j][2] = oacc[rt][j][3] = 0.f;
     }
-    int vref[NB];  // R_b as a scale byte; 0: none yet (the first block with larger ones sets it)
+    // 2^(127 - R_b), R_b as a scale byte; R_b = 0: none yet (the first block with larger scales
+    // sets it)
+    float vinv[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) vref[b] = 0;
+    for (int b = 0; b < NB; ++b) vinv[b] = __uint_as_float(254u << 23);
 
-    for (int k = 0; k < nb_w; ++k) {
-      const uint32_t st = it % NST;
-      if (!__all_sync(0xffffffffu, mbar_wait(&wbars[st], (it / NST) & 1u, p.wait_ns))) {
-        if (lane == 0) set_error(&p.hdr->error, PA_DEVERR_TIMEOUT);
-        timed_out = true;
-        for (int k2 = k + 1; k2 < min(nb_w, k + NST); ++k2)
-          mbar_wait(&wbars[(it + (k2 - k)) % NST], ((it + (k2 - k)) / NST) & 1u, p.wait_ns);
-        break;
-      }
-      const int phys = __shfl_sync(0xffffffffu, phys_lane, k);
-      if (phys >= 0) {
+    bool fresh = true;  // no block of the item is in O yet
+    // One block: `diag` if some row of the item does not see some of its keys.
+    auto tile_step = [&](int k, int st, auto diag_tag) {
+      constexpr bool diag = decltype(diag_tag)::value;
         const int key0 = (my_first + k * kDecodeWarps) * kBlockSize;
         const uint8_t* kt = wbuf + st * C::kStageBytes;
         const uint8_t* vt = kt + M::kTileBytes;
-        const bool diag = key0 + kBlockSize - 1 > I.pos_base;  // some row may not see some key
 
         // ---- S^T = K q^T ---------------------------------------------------------------
         float s[RT][4];  // (key lo, row 2qc), (key lo, row 2qc + 1), (key hi, ...)
@@ -242,12 +273,14 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
 #pragma unroll
               for (int rt = 0; rt < RT; ++rt) {
                 if (RT > 1 && 8 * rt >= I.rows) break;
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                float acc[4];
+                const uint4 qf = q_frag[(rt * NB + b) * 32];
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                   const uint32_t a[4] = {lo[g][2 * bb], hi[g][2 * bb], lo[g][2 * bb + 1],
                                          hi[g][2 * bb + 1]};
-                  mma_f16(acc, a, qf[rt][b][2 * g], qf[rt][b][2 * g + 1]);
+                  if (g == 0) mma_f16_zero(acc, a, qf.x, qf.y);
+                  else mma_f16(acc, a, qf.z, qf.w);
                 }
                 if (b == 0) {
                   s[rt][0] = acc[0] * sc_lo; s[rt][1] = acc[1] * sc_lo;
@@ -261,59 +294,6 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
           }
         }
 
-        // ---- softmax: P over S ------------------------------------------------------------
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          if (RT > 1 && 8 * rt >= I.rows) break;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[rt][i] *= row_scale[rt][i & 1];
-            if (diag && key0 + my_key + 8 * (i >> 1) > row_pos[rt][i & 1]) s[rt][i] = -CUDART_INF_F;
-          }
-          if constexpr (kScores) {
-            if (I.run * p.group <= p.score_rows) {  // one tile then: its rows are the run's
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int row = 8 * rt + 2 * qc + (i & 1);
-                if (row < I.rows)
-                  p.scores[((static_cast<int64_t>(I.s) * p.num_kv_heads + I.h) * p.score_rows + row) *
-                               p.score_stride + key0 + my_key + 8 * (i >> 1)] = s[rt][i];
-              }
-            }
-          }
-          const bool over = s[rt][0] > m_run[rt][0] + kLazyRescaleLog2 ||
-                            s[rt][2] > m_run[rt][0] + kLazyRescaleLog2 ||
-                            s[rt][1] > m_run[rt][1] + kLazyRescaleLog2 ||
-                            s[rt][3] > m_run[rt][1] + kLazyRescaleLog2;
-          if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float mx = fmaxf(s[rt][j], s[rt][2 + j]);
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              if (mx > m_run[rt][j] + kLazyRescaleLog2) {
-                const float alpha =
-                    m_run[rt][j] == -CUDART_INF_F ? 0.f : fast_exp2(m_run[rt][j] - mx);
-                m_run[rt][j] = mx;
-                l_run[rt][j] *= alpha;
-#pragma unroll
-                for (int n = 0; n < 2 * NB; ++n) {
-                  oacc[rt][n][j] *= alpha;
-                  oacc[rt][n][2 + j] *= alpha;
-                }
-              }
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float m_use = m_run[rt][j] == -CUDART_INF_F ? 0.f : m_run[rt][j];
-            s[rt][j] = fast_exp2(s[rt][j] - m_use);
-            s[rt][2 + j] = fast_exp2(s[rt][2 + j] - m_use);
-            l_run[rt][j] += s[rt][j] + s[rt][2 + j];
-          }
-        }
-
         // ---- V's scales: 2^(e - R_b) of this lane's two keys -----------------------------
         uint32_t vs[2];
 #pragma unroll
@@ -323,45 +303,151 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
             vs[i] = *reinterpret_cast<const uint32_t*>(vt + M::kCodeBytes + key * NB);
           else
             vs[i] = *reinterpret_cast<const uint16_t*>(vt + M::kCodeBytes + key * NB);
-          if (key0 + key > pos_last) vs[i] = 0u;  // a stale slot's bytes may be anything
         }
-        float fv[2][NB];
-        float fmax = 0.f;
+        uint32_t hidden[RT];  // bit i: element i of s[rt] is of a key that its row does not see
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const float inv = __uint_as_float(static_cast<uint32_t>(254 - vref[b]) << 23);
+        for (int rt = 0; rt < RT; ++rt) hidden[rt] = 0;
+        if (diag) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            fv[i][b] = e8m0_to_f32(vs[i], b) * inv;
-            fmax = fmaxf(fmax, fv[i][b]);
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              hidden[rt] |= (key0 + my_key + 8 * (i >> 1) > row_pos[rt][i & 1] ? 1u : 0u) << i;
+          // a stale slot's bytes may be anything
+          if (key0 + my_key > pos_last) vs[0] = 0u;
+          if (key0 + my_key + 8 > pos_last) vs[1] = 0u;
+        }
+        // the scores of short runs, for the key weights
+        if constexpr (kScores) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            if (I.run * p.group > p.score_rows) break;  // one tile otherwise: its rows are the run's
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = 8 * rt + 2 * qc + (i & 1);
+              if (row < I.rows)
+                p.scores[((static_cast<int64_t>(I.s) * p.num_kv_heads + I.h) * p.score_rows + row) *
+                             p.score_stride + key0 + my_key + 8 * (i >> 1)] =
+                    s[rt][i] * row_scale[rt][i & 1];
+            }
           }
         }
-        if (__any_sync(0xffffffffu, fmax > 128.f)) {
+
+        // ---- an item's first block: its first key's scores and scales are the first bases ------
+        if (fresh) {
+          uint32_t v0;
+          if constexpr (NB == 4) v0 = *reinterpret_cast<const uint32_t*>(vt + M::kCodeBytes);
+          else v0 = *reinterpret_cast<const uint16_t*>(vt + M::kCodeBytes);
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            const int lo = (vs[0] >> (8 * b)) & 255, hi = (vs[1] >> (8 * b)) & 255;
-            // (255 is NaN whatever the reference)
-            int top = max(lo == 255 ? 0 : lo, hi == 255 ? 0 : hi);
-            top = __reduce_max_sync(0xffffffffu, top);
-            if (top > vref[b] + 7) {
-              // O of the block moves to the new reference (253 at most: what is beyond has no
-              // finite value in fp32)
-              const int to = min(top, 253);
-              const float down =
-                  to - vref[b] > 126 ? 0.f
-                                     : __uint_as_float(static_cast<uint32_t>(127 - (to - vref[b])) << 23);
-              vref[b] = to;
-#pragma unroll
-              for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) oacc[rt][2 * b + t][i] *= down;
-            }
-            const float inv = __uint_as_float(static_cast<uint32_t>(254 - vref[b]) << 23);
-            fv[0][b] = e8m0_to_f32(vs[0], b) * inv;
-            fv[1][b] = e8m0_to_f32(vs[1], b) * inv;
+            const uint32_t e = (v0 >> (8 * b)) & 255u;  // (NaN: no reference yet)
+            vinv[b] = __uint_as_float((254u - (e == 255u ? 0u : min(e, 253u))) << 23);
           }
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float first = __shfl_sync(0xffffffffu, s[rt][j] * row_scale[rt][j], qc);
+              if (key0 <= row_pos[rt][j] && first > -FLT_MAX && first < FLT_MAX) m_run[rt][j] = first;
+            }
+        }
+
+        // ---- softmax: P and V's factors against the bases there are; where one of them has to
+        // move (rarely), it moves and they are computed again ------------------------------------
+        float fv[2][NB], pr[RT][4];
+#pragma unroll 1
+        for (bool again = true;; again = false) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            fv[0][b] = e8m0_to_f32(vs[0], b) * vinv[b];
+            fv[1][b] = e8m0_to_f32(vs[1], b) * vinv[b];
+          }
+          float fmax = fmaxf(fv[0][0], fv[1][0]), pmax = 0.f;
+#pragma unroll
+          for (int b = 1; b < NB; ++b) fmax = fmax3(fmax, fv[0][b], fv[1][b]);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            if (RT > 1 && 8 * rt >= I.rows) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              pr[rt][i] = fmaf(s[rt][i], row_scale[rt][i & 1], -m_run[rt][i & 1]);
+              if (diag && ((hidden[rt] >> i) & 1)) pr[rt][i] = -CUDART_INF_F;
+              pr[rt][i] = fast_exp2(pr[rt][i]);
+            }
+            pmax = fmax3(fmax3(pr[rt][0], pr[rt][1], pr[rt][2]), pr[rt][3], pmax);
+          }
+          if (!__any_sync(0xffffffffu, again && (fmax > 128.f || pmax > 256.f))) break;
+          // (O is rescaled only if something is in it)
+          if (__any_sync(0xffffffffu, pmax > 256.f)) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              if (RT > 1 && 8 * rt >= I.rows) break;
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                float mx = -CUDART_INF_F;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  if (!(diag && ((hidden[rt] >> (2 * i + j)) & 1)))
+                    mx = fmaxf(mx, s[rt][2 * i + j] * row_scale[rt][j]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                if (mx > m_run[rt][j] + kLazyRescaleLog2) {
+                  const float alpha = fast_exp2(m_run[rt][j] - mx);
+                  m_run[rt][j] = mx;
+                  l_run[rt][j] *= alpha;
+                  if (!fresh) {
+#pragma unroll
+                    for (int n = 0; n < 2 * NB; ++n) {
+                      oacc[rt][n][j] *= alpha;
+                      oacc[rt][n][2 + j] *= alpha;
+                    }
+                  }
+                }
+              }
+            }
+          }
+          if (__any_sync(0xffffffffu, fmax > 128.f)) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              const int e0 = (vs[0] >> (8 * b)) & 255, e1 = (vs[1] >> (8 * b)) & 255;
+              // the block's largest scale byte, NaN (255) aside
+              const int top = __reduce_max_sync(0xffffffffu, max(e0 == 255 ? 0 : e0, e1 == 255 ? 0 : e1));
+              const int ref = 254 - static_cast<int>(__float_as_uint(vinv[b]) >> 23);
+              if (top > ref + 7) {
+                // O of the block moves to the new reference (253 at most: what is beyond has no
+                // finite value in fp32)
+                const int to = min(top, 253);
+                vinv[b] = __uint_as_float(static_cast<uint32_t>(254 - to) << 23);
+                if (!fresh) {
+                  const float down =
+                      to - ref > 126
+                          ? 0.f
+                          : __uint_as_float(static_cast<uint32_t>(127 - (to - ref)) << 23);
+#pragma unroll
+                  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                      for (int i = 0; i < 4; ++i) oacc[rt][2 * b + t][i] *= down;
+                }
+              }
+              // A NaN block's codes are zeros: with a factor of 2^100, which is finite but makes
+              // any weight that counts infinite in f16, their products are NaN for every row that
+              // gives the key a weight and 0 for the others.
+              const uint32_t big =
+                  min(254, 354 - static_cast<int>(__float_as_uint(vinv[b]) >> 23)) << (8 * b);
+              if (e0 == 255) vs[0] = (vs[0] & ~(255u << (8 * b))) | big;
+              if (e1 == 255) vs[1] = (vs[1] & ~(255u << (8 * b))) | big;
+            }
+          }
+        }
+        fresh = false;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          if (RT > 1 && 8 * rt >= I.rows) break;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) l_run[rt][j] += pr[rt][j] + pr[rt][2 + j];
         }
 
         // ---- O^T += V^T P^T ---------------------------------------------------------------
@@ -371,7 +457,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
         for (int i = 0; i < 4; ++i) {
           const int key = ((i & 1) ? 4 + (qc ^ 1) : qc) + 8 * (i >> 1);
           if constexpr (NB == 4) {
-            const uint2 x = *reinterpret_cast<const uint2*>(vt + key * M::kRowBytes + quad * 8);
+            const uint2 x = *reinterpret_cast<const uint2*>(
+                vt + key * M::kRowBytes + ((quad * 8) ^ ((qc >> 1) << 5)));
             vw[i][0] = x.x; vw[i][1] = x.y;
           } else {
             vw[i][0] = *reinterpret_cast<const uint32_t*>(vt + key * M::kRowBytes + quad * 4);
@@ -393,15 +480,10 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
               if (RT > 1 && 8 * rt >= I.rows) break;
-              float pv[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                pv[i] = s[rt][i] * fv[i >> 1][b];
-                // a key that the row does not see adds nothing, whatever its scale
-                if (diag && s[rt][i] == 0.f) pv[i] = 0.f;
-              }
-              const uint32_t b0 = movmatrix_t(pack_f16x2(pv[0], pv[1]));
-              const uint32_t b1 = movmatrix_t(pack_f16x2(pv[2], pv[3]));
+              const uint32_t b0 =
+                  movmatrix_t(pack_f16x2(pr[rt][0] * fv[0][b], pr[rt][1] * fv[0][b]));
+              const uint32_t b1 =
+                  movmatrix_t(pack_f16x2(pr[rt][2] * fv[1][b], pr[rt][3] * fv[1][b]));
 #pragma unroll
               for (int t = 0; t < 2; ++t) {
                 const uint32_t a[4] = {ev[0][2 * bb + t], od[0][2 * bb + t], ev[1][2 * bb + t],
@@ -411,16 +493,31 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
             }
           }
         }
+    };
+    // (at least NST - 1 rounds, so that the copies reach the next item's first blocks)
+    const int rounds = max(nb_w, NST - 1);
+    for (int k = 0; k < rounds; ++k) {
+      cp_async_wait<NST - 2>();  // block k's copies have landed
+      __syncwarp();              // for every lane; and every lane has read the block before
+      {
+        const int ahead = k + NST - 1;
+        const int mine = __shfl_sync(0xffffffffu, tile_lane, ahead & 31);
+        const int nexts = __shfl_sync(0xffffffffu, tile_next, (ahead - rounds) & 31);
+        issue(ahead < nb_w ? mine
+              : ahead >= rounds && ahead - rounds < nb_next ? nexts : -1,
+              st == 0 ? NST - 1 : st - 1);
       }
-      __syncwarp();
-      ++it;
-      if (k + NST < nb_w) issue(k + NST);
+      if (k < nb_w && ((there >> k) & 1)) {
+        if ((my_first + k * kDecodeWarps + 1) * kBlockSize - 1 > I.pos_base)
+          tile_step(k, st, std::true_type());
+        else
+          tile_step(k, st, std::false_type());
+      }
+      st = st + 1 == NST ? 0 : st + 1;
     }
-    if (timed_out) it = 0;  // results are void; phase tracking no longer matters
 
-    // ---- per-warp state -> shared memory (this warp's own stages) --------------------------
-    __syncwarp();
-    float* so = reinterpret_cast<float*>(wbuf);  // [R][D]
+    // ---- per-warp state -> shared memory ------------------------------------------------------
+    float* so = scratch + warp * (C::kScratch / 4);  // [R][D]
     float* sm = so + R * D;                      // [R]
     float* sl = sm + R;                          // [R]
 #pragma unroll
@@ -440,7 +537,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
 #pragma unroll
         for (int n = 0; n < 2 * NB; ++n) {
           // 2^(R_b - 127)
-          const float up = __uint_as_float(static_cast<uint32_t>(vref[n >> 1]) << 23);
+          const float up = __uint_as_float((254u << 23) - __float_as_uint(vinv[n >> 1]));
           *reinterpret_cast<float2*>(so + row * D + 32 * (n >> 1) + 4 * quad + 2 * (n & 1)) =
               make_float2(oacc[rt][n][j] * up, oacc[rt][n][2 + j] * up);
         }
@@ -449,41 +546,49 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
     __syncthreads();
 
     // ---- merge the 4 warps and write the output or the partial ---------------------------
-    for (int e = threadIdx.x; e < I.rows * D; e += kDecodeWarps * 32) {
-      const int r = e / D, d = e - r * D;
+    for (int e = threadIdx.x; e < I.rows * (D / 4); e += kDecodeWarps * 32) {
+      const int r = e / (D / 4), d = 4 * (e % (D / 4));
       float mx = -CUDART_INF_F;
 #pragma unroll
       for (int w = 0; w < kDecodeWarps; ++w)
-        mx = fmaxf(mx, reinterpret_cast<const float*>(smem + w * C::kWarpBytes)[R * D + r]);
-      float lsum = 0.f, o = 0.f;
+        mx = fmaxf(mx, scratch[w * (C::kScratch / 4) + R * D + r]);
+      float lsum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kDecodeWarps; ++w) {
-        const float* wso = reinterpret_cast<const float*>(smem + w * C::kWarpBytes);
-        const float mw = wso[R * D + r];
-        // without a base (no key seen: zeros, or only NaN scores) the sums count as they are
-        const float f = mw == -CUDART_INF_F ? 1.f : fast_exp2(mw - mx);
+        const float* wso = scratch + w * (C::kScratch / 4);
+        const float f = fast_exp2(wso[R * D + r] - mx);  // (1 where no warp has a base: zeros or NaN)
         lsum += wso[R * D + R + r] * f;
-        o += wso[r * D + d] * f;
+        const float4 x = *reinterpret_cast<const float4*>(wso + r * D + d);
+        o[0] += x.x * f;
+        o[1] += x.y * f;
+        o[2] += x.z * f;
+        o[3] += x.w * f;
       }
-      const float val = lsum == 0.f ? 0.f : o / lsum;
-      const int t = I.t0 + r / p.group;
-      const int64_t orow = static_cast<int64_t>(t) * p.num_q_heads + I.h * p.group + r % p.group;
+      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = lsum == 0.f ? 0.f : o[i] * inv;
+      const int t = r / p.group;
+      const int64_t orow =
+          static_cast<int64_t>(I.t0 + t) * p.num_q_heads + I.h * p.group + (r - t * p.group);
       const float lse = lsum == 0.f ? -CUDART_INF_F : mx + __log2f(lsum);
       if (I.nparts == 1) {
         if (p.out_bf16)
-          reinterpret_cast<__nv_bfloat16*>(p.out)[orow * D + d] = __float2bfloat16_rn(val);
+          *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * D + d) =
+              make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
         else
-          reinterpret_cast<float*>(p.out)[orow * D + d] = val;
+          *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + orow * D + d) =
+              make_float4(o[0], o[1], o[2], o[3]);
         if (p.lse && d == 0) p.lse[orow] = lse;
       } else {
         const int64_t prow = orow * p.pmax + I.part;
-        p.part_o[prow * D + d] = val;
+        *reinterpret_cast<float4*>(p.part_o + prow * D + d) = make_float4(o[0], o[1], o[2], o[3]);
         if (d == 0) p.part_lse[prow] = lse;
       }
     }
-    __syncthreads();
-    fence_proxy_async_smem();  // generic accesses to the stages before the next copies
-    cur ^= 1;
+    slot = next_slot;
+    buf ^= 1;
+    nb_w = nb_next;
+    tile_lane = tile_next;
   }
   if (p.span && threadIdx.x == 0)
     atomicMax(reinterpret_cast<unsigned long long*>(p.span) + 1,

@@ -295,24 +295,6 @@ def test_mxfp4_bad_block_ids_and_lengths():
     assert pa.check_error(ws, raise_on_error=False) == 0x4
 
 
-def test_mxfp4_wait_that_expires_reports_a_timeout():
-    import paged_kv_cache_286_gb300 as pa
-    c = Case([100, 64, 600], [1, 1, 1], 4, 2, 128, "mxfp4", seed=11)
-    t, ctx, qsl = c.dev()
-    ws = c.workspace(pa)
-    L = pa.library()
-    good = pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, **c.hints())
-    try:
-        L.pa_set_wait_limit_ns(20_000_000)
-        L.pa_test_skip_one_copy(1)
-        pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, **c.hints())
-        assert pa.check_error(ws, raise_on_error=False) & 0x8
-    finally:
-        L.pa_test_skip_one_copy(0)
-        L.pa_set_wait_limit_ns(0)
-    assert torch.equal(pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, **c.hints()), good)
-
-
 # ---------------------------------------------------------------------------------------------
 # accumulated key weights
 # ---------------------------------------------------------------------------------------------
