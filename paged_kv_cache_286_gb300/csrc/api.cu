@@ -230,6 +230,20 @@ WsLayout workspace_layout(int32_t S, int32_t T, int32_t Hq, int32_t Hkv, int32_t
   return w;
 }
 
+size_t mx_stage_bytes(int32_t S, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_ctx,
+                      int32_t max_q) {
+  if (S <= 0 || T <= 0 || Hkv <= 0 || Hq < Hkv || D <= 0) return 0;
+  const int64_t G = Hq / Hkv;
+  if (max_q * G <= kMxMaxRows) return 0;
+  const int64_t seqs = std::min<int64_t>(S, T / (kMxMaxRows / G + 1));  // with runs that long
+  const int64_t blocks = (std::max(max_ctx, 1) + int64_t(kBlockSize) - 1) / kBlockSize;
+  const int64_t block_bytes = int64_t(Hkv) * kBlockSize * D * 4;  // K and V
+  const int64_t cap = (int64_t(256) << 20) / block_bytes;
+  return static_cast<size_t>(std::min(seqs * blocks, cap) * block_bytes) +
+         ((sizeof(int32_t) * (size_t(S) + 1) + 255) & ~size_t(255)) +
+         ((sizeof(int32_t) * size_t(S) * size_t(blocks) + 255) & ~size_t(255));
+}
+
 KeyWeightsLayout key_weights_layout(int32_t S, int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
                                     int32_t max_ctx, int32_t max_q) {
   KeyWeightsLayout w{};
@@ -437,7 +451,9 @@ size_t pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_tokens, int32
   (void)block_size;
   return pa::workspace_layout(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
                               max_context_len, max_query_len)
-      .total;
+             .total +
+         pa::mx_stage_bytes(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
+                            max_context_len, max_query_len);
 }
 
 struct Scores {  // where the split-KV path writes its scores (DecodeParams)
@@ -445,7 +461,31 @@ struct Scores {  // where the split-KV path writes its scores (DecodeParams)
   int32_t rows = 0, stride = 0;
 };
 
-// Attention of one step; `lse` ([num_q_tokens][num_q_heads], or NULL) also receives the rows'
+// The staging area of MXFP4 steps in what the workspace has beyond `used` bytes.
+static pa::MxStage stage_area(uint8_t* ws, size_t used, size_t bytes, int32_t S, int32_t Hkv,
+                              int32_t D, int32_t max_ctx) {
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  pa::MxStage a;
+  a.table_stride = (max_ctx - 1) / pa::kBlockSize + 1;
+  size_t off = up(used);
+  const size_t prefix = off;
+  off = up(off + sizeof(int32_t) * (size_t(S) + 1));
+  const size_t table = off;
+  off = up(off + sizeof(int32_t) * size_t(S) * size_t(a.table_stride));
+  const size_t block = size_t(Hkv) * pa::kBlockSize * size_t(D) * 2;  // of K or V
+  if (off + 2 * block > bytes) return pa::MxStage{};
+  const int64_t rows = int64_t(Hkv) * pa::kBlockSize;  // of a block: TMA's row index is 32 bits
+  a.capacity = static_cast<int32_t>(
+      std::min<int64_t>(static_cast<int64_t>((bytes - off) / (2 * block)), INT32_MAX / rows));
+  a.prefix = reinterpret_cast<int32_t*>(ws + prefix);
+  a.table = reinterpret_cast<int32_t*>(ws + table);
+  a.k = ws + off;
+  a.v = ws + off + block * size_t(a.capacity);
+  return a;
+}
+
+// Attention of one step.  `used_bytes` of the workspace are the caller's (0: none past
+// pa_attention's own layout); `lse` ([num_q_tokens][num_q_heads], or NULL) also receives the rows'
 // log-sum-exps in the log2 domain.
 static pa_status attend(const void* q, int32_t num_q_tokens, const void* k_cache,
                         const void* v_cache, const pa_cache_desc* cache,
@@ -454,7 +494,7 @@ static pa_status attend(const void* q, int32_t num_q_tokens, const void* k_cache
                         int32_t num_seqs, int32_t max_context_len, int32_t max_query_len,
                         int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
                         void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes,
-                        cudaStream_t stream, float* lse, const Scores& scores) {
+                        cudaStream_t stream, size_t used_bytes, float* lse, const Scores& scores) {
   bool nothing = false;
   pa_status st = pa::check_attention_args(
       q, num_q_tokens, k_cache, v_cache, cache, block_tables, max_blocks_per_seq, context_lens,
@@ -470,6 +510,7 @@ static pa_status attend(const void* q, int32_t num_q_tokens, const void* k_cache
   if (workspace_bytes < ws.total)
     return fail(PA_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes,
                 ws.total);
+  used_bytes = std::max(used_bytes, ws.total);
   pa::PoolMaps maps;
   // boxes of one or two kv heads' rows (two only for single-token E4M3 decode, where no
   // prefill tile reads these maps)
@@ -489,7 +530,25 @@ static pa_status attend(const void* q, int32_t num_q_tokens, const void* k_cache
     if ((st = encode_pool_tile_map(&maps.v4, v_cache, *cache)) != PA_OK) return st;
     maps.has_k4 = true;
   }
-  if (use_prefill) {
+  pa::MxStage stage;
+  if (cache->cache_dtype == PA_MXFP4 && max_query_len * int64_t(G) > pa::kMxMaxRows &&
+      pa::prefill_geometry(num_q_heads, num_kv_heads))
+    stage = stage_area(static_cast<uint8_t*>(workspace), used_bytes, workspace_bytes, num_seqs,
+                       num_kv_heads, head_dim, max_context_len);
+  if (stage.capacity > 0) {
+    pa_cache_desc area = *cache;
+    area.cache_dtype = PA_BF16;
+    area.num_blocks = stage.capacity;
+    if (head_dim == 128) {
+      if ((st = encode_pool_tile_map(&maps.k4, stage.k, area)) != PA_OK) return st;
+      if ((st = encode_pool_tile_map(&maps.v4, stage.v, area)) != PA_OK) return st;
+      maps.has_k4 = true;
+    } else {
+      if ((st = encode_pool_map(&maps.k2, stage.k, area)) != PA_OK) return st;
+      if ((st = encode_pool_map(&maps.v2, stage.v, area)) != PA_OK) return st;
+    }
+  }
+  if (use_prefill || stage.capacity > 0) {
     if ((st = encode_q_map(&maps.q3, q, num_q_tokens, num_q_heads, head_dim, G)) != PA_OK)
       return st;
     maps.has_q3 = true;
@@ -508,6 +567,7 @@ static pa_status attend(const void* q, int32_t num_q_tokens, const void* k_cache
   a.scores = scores.data;
   a.score_rows = scores.rows;
   a.score_stride = scores.stride;
+  a.stage = stage;
   cudaError_t e = pa::launch_attention(a, ws, maps, use_prefill, g_before, g_after);
   if (e != cudaSuccess) return cuda_fail(e, "pa_attention launch");
   return PA_OK;
@@ -525,7 +585,7 @@ pa_status pa_attention(const void* q, int32_t num_q_tokens, const void* k_cache,
   return attend(q, num_q_tokens, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
                 context_lens, query_start_loc, num_seqs, max_context_len, max_query_len,
                 num_q_heads, num_kv_heads, head_dim, scale, out, out_dtype, workspace,
-                workspace_bytes, stream, nullptr, Scores{});
+                workspace_bytes, stream, 0, nullptr, Scores{});
 }
 
 size_t pa_attention_key_weights_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
@@ -535,7 +595,9 @@ size_t pa_attention_key_weights_workspace_size(int32_t num_seqs, int32_t num_q_t
   (void)block_size;
   return pa::key_weights_layout(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
                                 max_context_len, max_query_len)
-      .total;
+             .total +
+         pa::mx_stage_bytes(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
+                            max_context_len, max_query_len);
 }
 
 pa_status pa_attention_key_weights(
@@ -572,7 +634,7 @@ pa_status pa_attention_key_weights(
   st = attend(q, num_q_tokens, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
               context_lens, query_start_loc, num_seqs, max_context_len, max_query_len, num_q_heads,
               num_kv_heads, head_dim, scale, out, out_dtype, workspace, workspace_bytes, stream,
-              lse, scores);
+              ws.total, lse, scores);
   if (st != PA_OK) return st;
   pa::KeyWeightsArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(q);

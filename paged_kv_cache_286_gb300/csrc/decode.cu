@@ -43,9 +43,9 @@ namespace pa {
 
 // Prefill-path items of one sequence: one per (kv head, 128-row tile of tokens x heads, key
 // split of the tile).
-__device__ __forceinline__ int prefill_items_of(const DecodeParams& p, int n, int L) {
+__device__ __forceinline__ int prefill_items_of(const DecodeParams& p, int s, int n, int L) {
   bool bad;
-  if (decode_items_of(p, n, L, &bad) != 0 || bad || n <= 0) return 0;
+  if (decode_items_of(p, s, n, L, &bad) != 0 || bad || n <= 0) return 0;
   const int tpt = 128 / p.group;
   return p.num_kv_heads * ceil_div(n, tpt) * prefill_splits(n, L, p.group, p.pmax);
 }
@@ -80,9 +80,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const DecodeParams p) {
       const int n = p.qsl[s + 1] - p.qsl[s];
       const int L = p.context_lens[s];
       bool bad;
-      cnt[0] = decode_items_of(p, n, L, &bad);
+      cnt[0] = decode_items_of(p, s, n, L, &bad);
       if (bad) set_error(&p.hdr->error, PA_DEVERR_LENGTHS);
-      cnt[1] = prefill_items_of(p, n, L);
+      cnt[1] = prefill_items_of(p, s, n, L);
       // rows the merge combines: split-KV sequences of two or more partitions, and prefill
       // runs whose tiles are split along the keys
       cnt[2] = ((cnt[0] > 0 && partitions_of(p, L) > 1) ||
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const DecodeParams p) {
         c = sort_cnt[r];
       } else if (r < R) {
         const int s = p.pf_order[r];
-        c = prefill_items_of(p, p.qsl[s + 1] - p.qsl[s], p.context_lens[s]);
+        c = prefill_items_of(p, s, p.qsl[s + 1] - p.qsl[s], p.context_lens[s]);
       }
       int x = c;
 #pragma unroll
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const DecodeParams p) {
   float t = CUDART_INF_F;
   if (search && P <= pmax) {
     const float tp = fmaxf(w_pf / P, longest);
-    const float rate = fminf(kHbmBytesPerUs, float(p.sms - P) * kDecodeSmBytesPerUs);
+    const float rate = fminf(kHbmBytesPerUs, float(p.sms - P) * p.sm_rate);
     t = fmaxf(tp, rate > 0.f ? bytes / rate : CUDART_INF_F);
   }
   __shared__ float red_t[32];
@@ -955,7 +955,7 @@ __global__ void __launch_bounds__(256, 4) merge_kernel(const DecodeParams p) {
     const int n = p.qsl[s + 1] - t0, L = p.context_lens[s];
     const int64_t rid = static_cast<int64_t>(t0) * p.num_q_heads + local;
     bool bad;
-    const int nparts = decode_items_of(p, n, L, &bad) > 0 ? partitions_of(p, L)
+    const int nparts = decode_items_of(p, s, n, L, &bad) > 0 ? partitions_of(p, L)
                                                          : prefill_splits(n, L, p.group, p.pmax);
     merge_row<D>(p, rid, nparts, lane);
   }
@@ -1013,11 +1013,15 @@ int decode_heads_per_item(const pa_cache_desc& c, int32_t num_q_heads, int32_t n
              : 1;
 }
 
-bool prefill_path_enabled(const pa_cache_desc& c, int32_t num_q_heads, int32_t num_kv_heads) {
+bool prefill_geometry(int32_t num_q_heads, int32_t num_kv_heads) {
   const int G = num_q_heads / num_kv_heads;
+  return G >= 1 && G <= kRowsPerTile && 128 % G == 0;
+}
+
+bool prefill_path_enabled(const pa_cache_desc& c, int32_t num_q_heads, int32_t num_kv_heads) {
   const bool built = (c.cache_dtype == PA_BF16 && (c.head_dim == 128 || c.head_dim == 64)) ||
                      (c.cache_dtype == PA_FP8_E4M3 && c.head_dim == 128);
-  return built && G >= 1 && G <= kRowsPerTile && 128 % G == 0;
+  return built && prefill_geometry(num_q_heads, num_kv_heads);
 }
 
 cudaError_t launch_attention(const AttnArgs& a, const WsLayout& ws, const PoolMaps& maps,
@@ -1078,7 +1082,9 @@ cudaError_t launch_attention(const AttnArgs& a, const WsLayout& ws, const PoolMa
   const int dec_q = std::min(a.max_query_len, p.decode_max_query);
   const bool mixed = prefill && routes_to_prefill(a.max_query_len, p.group);
   const bool rt2 = p.group > 8 || (!mixed && static_cast<int64_t>(dec_q) * p.group > 8);
-  p.rows_per_tile = mx ? 8 * mx_row_tiles(a.max_query_len, p.group) : rt2 ? 16 : 8;
+  // MXFP4: tiles for the longest run, unless the long runs are staged for the prefill tiles
+  const bool staged = a.stage.capacity > 0;
+  p.rows_per_tile = mx ? (staged ? 8 : 8 * mx_row_tiles(a.max_query_len, p.group)) : rt2 ? 16 : 8;
   p.lse = a.lse;
   p.scores = a.scores;
   p.score_rows = a.score_rows;
@@ -1091,6 +1097,12 @@ cudaError_t launch_attention(const AttnArgs& a, const WsLayout& ws, const PoolMa
   p.kv_tile_bytes = mx ? 2 * a.head_dim * 17 / 2 : 2 * kBlockSize * a.head_dim * (fp8 ? 1 : 2);
   p.span = a.span;
 
+  p.sm_rate = mx ? kMxSmBytesPerUs : kDecodeSmBytesPerUs;
+
+  if (staged) {
+    p.stage_pre = a.stage.prefix;
+    if ((e = launch_mx_stage_plan(a, p)) != cudaSuccess) return e;
+  }
   e = launch_dependent(plan_kernel, dim3(1), dim3(1024), 0, a.stream, p);
   if (e != cudaSuccess) return e;
   // The prefill tiles (tensor pipe, key slices mostly from L2) and the split-KV decode (HBM)
@@ -1099,7 +1111,19 @@ cudaError_t launch_attention(const AttnArgs& a, const WsLayout& ws, const PoolMa
   // the split-KV kernel launch; its CTAs fill the SMs the prefill left free at once (and the
   // others as prefill CTAs end), and wait for the prefill kernel only before they exit.  Both
   // only read what the plan and the append wrote, and write disjoint output rows.
-  if (prefill) {
+  if (staged) {
+    // the staged sequences as a bf16 pool of their own
+    if ((e = launch_mx_stage(a, p)) != cudaSuccess) return e;
+    AttnArgs b = a;
+    b.cache.cache_dtype = PA_BF16;
+    b.cache.num_blocks = a.stage.capacity;
+    b.block_tables = a.stage.table;
+    b.max_blocks_per_seq = a.stage.table_stride;
+    PrefillScratch scratch{p.part_lse, p.part_o, p.pmax};
+    if ((e = launch_prefill(b, p.pf_item_start, p.pf_order, p.hdr, maps, scratch)) != cudaSuccess)
+      return e;
+    p.wait_at_end = 1;
+  } else if (prefill) {
     PrefillScratch scratch{p.part_lse, p.part_o, p.pmax};
     if ((e = launch_prefill(a, p.pf_item_start, p.pf_order, p.hdr, maps, scratch)) !=
         cudaSuccess)

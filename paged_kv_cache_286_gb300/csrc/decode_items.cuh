@@ -48,6 +48,9 @@ struct DecodeParams {
                            // up to score_rows rows (row = token x group + head), or NULL
   int32_t score_rows;
   int32_t score_stride;
+  const int32_t* stage_pre;  // [S + 1] staged blocks (mx_stage.cu): sequences that have some go to
+                             // the prefill tiles, and no others; NULL: by decode_max_query / _rows
+  float sm_rate;             // cost model: HBM bytes per microsecond of one SM's split-KV CTAs
 };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -57,8 +60,9 @@ __device__ __forceinline__ int partitions_of(const DecodeParams& p, int L) {
   return ceil_div(ceil_div(L, kBlockSize), p.pblk);
 }
 
-// Items of one sequence on the decode path (0 if it belongs to the prefill path or is invalid).
-__device__ __forceinline__ int decode_items_of(const DecodeParams& p, int n, int L, bool* bad) {
+// Items of sequence s on the decode path (0 if it belongs to the prefill path or is invalid).
+__device__ __forceinline__ int decode_items_of(const DecodeParams& p, int s, int n, int L,
+                                               bool* bad) {
   *bad = false;
   if (n <= 0) {
     *bad = (n < 0);
@@ -69,7 +73,9 @@ __device__ __forceinline__ int decode_items_of(const DecodeParams& p, int n, int
     *bad = true;
     return 0;
   }
-  if (n > p.decode_max_query || n * p.group > p.decode_max_rows) return 0;
+  if (p.stage_pre ? p.stage_pre[s + 1] > p.stage_pre[s]
+                  : n > p.decode_max_query || n * p.group > p.decode_max_rows)
+    return 0;
   const int tpt = p.rows_per_tile / (p.group * p.heads_per_item);  // query tokens per tile
   const int qtiles = ceil_div(n, tpt);
   const int nparts = partitions_of(p, L);

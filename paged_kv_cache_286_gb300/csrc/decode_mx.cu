@@ -82,7 +82,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
   // with bit 1 set are swapped on the way in, which makes V's loads free of conflicts.
   const int my_key = (quad & 1) ? 4 + ((quad >> 1) ^ 1) : quad >> 1;
 
-  grid_dependency_wait();
+  // after the prefill tiles (which waited for the plan) it starts beside them and waits for them
+  // only before it ends
+  if (!p.wait_at_end) grid_dependency_wait();
   if (p.span && threadIdx.x == 0)
     atomicMin(reinterpret_cast<unsigned long long*>(p.span),
               static_cast<unsigned long long>(global_ns()));
@@ -321,14 +323,14 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
         if constexpr (kScores) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            if (I.run * p.group > p.score_rows) break;  // one tile otherwise: its rows are the run's
+            if (I.run * p.group > p.score_rows) break;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int row = 8 * rt + 2 * qc + (i & 1);
               if (row < I.rows)
-                p.scores[((static_cast<int64_t>(I.s) * p.num_kv_heads + I.h) * p.score_rows + row) *
-                             p.score_stride + key0 + my_key + 8 * (i >> 1)] =
-                    s[rt][i] * row_scale[rt][i & 1];
+                p.scores[((static_cast<int64_t>(I.s) * p.num_kv_heads + I.h) * p.score_rows +
+                          I.qt * (R / p.group) * p.group + row) * p.score_stride +
+                         key0 + my_key + 8 * (i >> 1)] = s[rt][i] * row_scale[rt][i & 1];
             }
           }
         }
@@ -593,6 +595,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT>::kCtas)
   if (p.span && threadIdx.x == 0)
     atomicMax(reinterpret_cast<unsigned long long*>(p.span) + 1,
               static_cast<unsigned long long>(global_ns()));
+  if (p.wait_at_end) grid_dependency_wait();
 }
 
 template <int D, int RT, bool kScores = false>
@@ -614,7 +617,7 @@ static cudaError_t run_mx(const AttnArgs& a, int pmax, const DecodeParams& p) {
                           static_cast<const uint8_t*>(a.v_cache), p);
 }
 
-// Row tiles of an item: enough for the longest run, at most 32 rows.
+// Row tiles of an item: enough for the longest run, at most kMxMaxRows rows.
 int mx_row_tiles(int32_t max_query_len, int32_t group) {
   const int64_t rows = static_cast<int64_t>(max_query_len) * group;
   return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;

@@ -32,6 +32,7 @@ constexpr float kTileSliceUs = 1.34f;
 constexpr float kTileItemUs = 3.5f;
 constexpr float kDecodeSmBytesPerUs = 7.5e4f;
 constexpr float kHbmBytesPerUs = 6.7e6f;
+constexpr float kMxSmBytesPerUs = 2.8e4f;  // MXFP4's split-KV CTAs
 
 // A load that bypasses L1: for values another kernel of the stream wrote before this kernel
 // was launched, read without a dependency wait in between.
@@ -44,6 +45,8 @@ constexpr int kRowsPerTile = 8;           // (query token x GQA head) rows of a 
 constexpr int kDecodeMaxGroup = 16;      // q heads per kv head: up to 16 rows of one item
 constexpr int kDecodeMaxQuery = 16;       // sequences with n_s above this use the prefill path,
 constexpr int kDecodeMaxRows = 16;        // and so do those with more n_s x G rows than this
+
+constexpr int kMxMaxRows = 32;            // rows of the largest tile of the MXFP4 split-KV kernel
 
 // Whether a query run of n tokens with G heads per kv head is served by the prefill-tile
 // kernel (when that kernel is built for the pool): more rows than one 16-row decode tile holds

@@ -29,6 +29,17 @@ cudaError_t launch_info(Kernel kern, int threads, int smem_bytes, LaunchInfo* ou
   return launch_info_impl(reinterpret_cast<const void*>(kern), threads, smem_bytes, out);
 }
 
+// Where the keys and values of MXFP4 sequences with long query runs are written out as bf16 for
+// the prefill tiles (mx_stage.cu); capacity 0: nowhere.
+struct MxStage {
+  int32_t* prefix = nullptr;   // [S + 1] prefix sums of the staged sequences' blocks
+  int32_t* table = nullptr;    // [S][table_stride] block tables into the area
+  void* k = nullptr;           // [capacity][Hkv][16][D] bf16
+  void* v = nullptr;
+  int32_t capacity = 0;        // blocks
+  int32_t table_stride = 0;
+};
+
 // Everything pa_attention received, after host validation.
 struct AttnArgs {
   const void* q;
@@ -61,6 +72,7 @@ struct AttnArgs {
   float* scores = nullptr;          // scores of the split-KV path's rows, or NULL (DecodeParams)
   int32_t score_rows = 0;
   int32_t score_stride = 0;
+  MxStage stage;                    // MXFP4 pools with long query runs
 };
 
 // Workspace carve-up; a pure function of the step's shape (see workspace_layout).
@@ -76,6 +88,13 @@ struct WsLayout {
   int32_t pblk;       // blocks per KV partition
   int32_t pmax;       // partitions per sequence at most
 };
+
+// Bytes beyond the layouts above in which an MXFP4 step with long query runs stages their keys and
+// values: what they can be at most, but no more than 256 MiB (sequences past that take the split-KV
+// kernel).  0 for steps without such runs.
+size_t mx_stage_bytes(int32_t num_seqs, int32_t num_q_tokens, int32_t num_q_heads,
+                      int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
+                      int32_t max_query_len);
 
 WsLayout workspace_layout(int32_t num_seqs, int32_t num_q_tokens, int32_t num_q_heads,
                           int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
@@ -146,6 +165,7 @@ cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, const pa_cache_desc
 // then take boxes of 16 x that many rows.
 int decode_heads_per_item(const pa_cache_desc& c, int32_t num_q_heads, int32_t num_kv_heads,
                           int32_t max_query_len);
+bool prefill_geometry(int32_t num_q_heads, int32_t num_kv_heads);  // its heads' part of that
 bool prefill_path_enabled(const pa_cache_desc& c, int32_t num_q_heads, int32_t num_kv_heads);
 
 // `qmap` (3-D view of q) is needed only when the prefill path is enabled and
@@ -198,6 +218,9 @@ cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t stream);
 struct DecodeParams;
 // MXFP4 pools (decode_mx.cu): row tiles of 8 rows of an item, and the attention kernel.
 int mx_row_tiles(int32_t max_query_len, int32_t group);
+// Sequences with more rows than its tiles: bf16 copies of their keys and values.
+cudaError_t launch_mx_stage_plan(const AttnArgs& a, const DecodeParams& p);
+cudaError_t launch_mx_stage(const AttnArgs& a, const DecodeParams& p);
 cudaError_t launch_decode_mx(const AttnArgs& a, int pmax, const DecodeParams& p);
 
 struct WsHeader;

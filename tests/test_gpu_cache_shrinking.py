@@ -264,6 +264,38 @@ def test_mxfp4_runs(qlens, ctx, hq, hkv, d):
         check_mx(c, out)
 
 
+@pytest.mark.parametrize("d,hq,hkv", [(128, 8, 2), (64, 4, 4)])
+@pytest.mark.parametrize("share", [1.0, 0.5, 0.0])
+def test_mxfp4_chunks_with_room_to_stage_all_some_and_none(d, hq, hkv, share):
+    """Long runs go to the prefill tiles through a bf16 copy in what the workspace has past the
+    attention's own part, and to the split-KV kernel where it has no room for them."""
+    import paged_kv_cache_286_gb300 as pa
+    qlens, ctx = [60, 1, 200, 3, 45, 7], [500, 900, 200, 77, 1300, 700]
+    c = Case(ctx, qlens, hq, hkv, d, "mxfp4", seed=31 + d)
+    t, ctx, qsl = c.dev()
+    ws = c.workspace(pa)
+    group = hq // hkv
+    blocks = min(len(qlens), sum(qlens) // (32 // group + 1)) * -(-1300 // BS)
+    ws = ws[:ws.numel() - int((1 - share) * blocks) * hkv * BS * d * 4]
+    ws[256:] = 0xFF
+    before = np.random.default_rng(1).random((6, hkv, 1300)).astype(np.float32)
+    for dt in (torch.float32, torch.bfloat16):
+        out = pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, out_dtype=dt, **c.hints())
+        assert pa.check_error(ws) == 0
+        check_mx(c, out)
+    W = torch.from_numpy(before).cuda()
+    ws = c.workspace(pa, True)
+    ws = ws[:ws.numel() - int((1 - share) * blocks) * hkv * BS * d * 4]
+    pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, ctx, qsl, W, ws, **c.hints())
+    assert pa.check_error(ws) == 0
+    check_weights(c, before, W.cpu().numpy(), list(range(6)), 1.0)
+    good = pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, **c.hints())
+    t[2, 3] = 10 ** 6                                    # a bad block: its sequence's rows are lost
+    out = pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, **c.hints())
+    assert pa.check_error(ws, raise_on_error=False) == 0x1
+    assert torch.equal(out[:61], good[:61]) and torch.equal(out[261:], good[261:])
+
+
 def test_mxfp4_nan_block_reaches_only_the_rows_that_see_it():
     import paged_kv_cache_286_gb300 as pa
     for which in ("k", "v"):
