@@ -5,10 +5,14 @@
 //   W[j] <- decay * W[j] + sum over the rows that see j of 2^(s_j - lse_row),
 // s_j = scale * log2(e) * q . k_j, i.e. the sum of the softmax weights that j received.
 //
-//  * The keys stay: a warp holds 32 keys of one kv head as MMA fragments (M = keys, two m16 tiles)
-//    and the rows of the group pass through shared memory as the N operand, eight at a time, so
-//    a key's sum over rows stays in the lanes that own it and is written once, in a fixed order:
-//    no atomics, the same bits every time.  Keys are read once, whatever the number of rows.
+//  * Decode tokens and short verify runs: the attention's split-KV kernel writes its scores (4 bytes
+//    per row and key) and kw_finish_kernel reads them; K is not read again.
+//  * Longer runs, whose scores would be more bytes than K: the keys stay and the rows pass.  A warp
+//    holds 32 keys of one kv head as MMA fragments (M = keys, two m16 tiles) and the rows of the
+//    group pass through shared memory as the N operand, eight at a time, so a key's sum over rows
+//    stays in the lanes that own it and is written once, in a fixed order: no atomics, the same
+//    bits every time.  A cluster of four CTAs shares the rows of 128 keys, so that a single chunk
+//    (512 tokens after 2,048: 160 items) fills the GPU.
 //  * The log-sum-exp is known, so there is no running maximum: a score costs one FMA, one 2^x and
 //    one add.
 //  * Every pool type becomes bf16 fragments, exactly (E4M3 has four significant bits, E2M1 times
@@ -26,9 +30,10 @@ namespace pa {
 
 namespace {
 
-constexpr int kKwWarps = 4;
-constexpr int kKwKeys = 32 * kKwWarps;  // keys of an item
-constexpr int kKwRows = 64;             // rows staged in shared memory at a time
+constexpr int kKwKeys = 128;    // keys of an item: four groups of 32
+constexpr int kKwWarps = 8;     // key group x half of the staged rows
+constexpr int kKwRows = 64;     // rows staged in shared memory at a time
+constexpr int kKwCluster = 4;   // CTAs that share an item's rows
 
 enum class Pool { kBf16, kE4m3, kMx };
 
@@ -71,7 +76,7 @@ __global__ void __launch_bounds__(kFinThreads) kw_finish_kernel(const KeyWeights
   if (!ok) return;
   const int t0 = a.qsl[s], n = a.qsl[s + 1] - t0, L = a.context_lens[s];
   const int G = a.num_q_heads / a.num_kv_heads;
-  if (n * G > a.score_rows) return;
+  if (n * G > a.score_rows || (blockIdx.y && blockIdx.y * kFinShare >= L)) return;
   if (threadIdx.x < n * G)
     s_lse[threadIdx.x] = a.lse[static_cast<int64_t>(t0 + threadIdx.x / G) * a.num_q_heads + h * G +
                                threadIdx.x % G];
@@ -82,7 +87,7 @@ __global__ void __launch_bounds__(kFinThreads) kw_finish_kernel(const KeyWeights
                                    a.score_stride;
   const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
   const int groups = (L + 3) / 4;
-  const int share = (groups + gridDim.y - 1) / gridDim.y;
+  const int share = max(kFinShare / 4, static_cast<int>((groups + gridDim.y - 1) / gridDim.y));
   const int end = min(groups, share * (static_cast<int>(blockIdx.y) + 1));
   for (int g = share * blockIdx.y + threadIdx.x; g < end; g += kFinThreads) {
     const int key = 4 * g;
@@ -144,21 +149,75 @@ __global__ void __launch_bounds__(1024) kw_plan_kernel(const KeyWeightsArgs a) {
   if (bits) set_error(a.err, bits);
 }
 
+// 8 dims of a key (32 c + 8 qc ..) as bf16 pairs, exactly.
 template <Pool kPool, int D>
-__global__ void __launch_bounds__(kKwWarps * 32, 4) key_weights_kernel(const KeyWeightsArgs a) {
+__device__ __forceinline__ void load_dims(const uint8_t* __restrict__ k_cache, int64_t tile,
+                                          int off, int c, int qc, uint32_t (&w)[4]) {
+  constexpr int NC = D / 32;
+  if constexpr (kPool == Pool::kBf16) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(
+        k_cache + ((tile * kBlockSize + off) * D + 32 * c + 8 * qc) * 2));
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+  } else if constexpr (kPool == Pool::kE4m3) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(
+        k_cache + (tile * kBlockSize + off) * D + 32 * c + 8 * qc));
+    const uint32_t u[2] = {x.x, x.y};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float f0, f1;
+      e4m3x2_to_f32x2(static_cast<uint16_t>(u[j >> 1] >> (16 * (j & 1))), f0, f1);
+      w[j] = pack_bf16x2(f0, f1);
+    }
+  } else {
+    const uint8_t* t = k_cache + tile * Mx<D>::kTileBytes;
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(t + off * Mx<D>::kRowBytes);
+    const uint32_t codes = __ldg(src + 2 * qc * NC + c) |
+                           (static_cast<uint32_t>(__ldg(src + (2 * qc + 1) * NC + c)) << 16);
+    const float sc = e8m0_to_f32(__ldg(t + Mx<D>::kCodeBytes + off * NC + c), 0);
+    uint32_t f[4];
+    e2m1x8_to_f16x2x4(codes, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&f[j]));
+      w[j] = pack_bf16x2(y.x * sc, y.y * sc);
+    }
+  }
+}
+
+template <int D>
+constexpr int kKwStride = D * 2 + 16;  // bytes of a row in shared memory: ldmatrix without conflicts
+template <int D>
+constexpr int kKwSmem = (kKwKeys + 2 * kKwRows) * kKwStride<D>;
+
+// A cluster has an item (128 keys of a kv head); its CTAs take the item's 64-row tiles in turn, and
+// their sums meet through distributed shared memory, CTA 0's first.
+template <Pool kPool, int D>
+__global__ void __cluster_dims__(kKwCluster, 1, 1) __launch_bounds__(kKwWarps * 32, 2)
+    key_weights_kernel(const KeyWeightsArgs a) {
   constexpr int KS = D / 16;               // MMA k-steps
-  constexpr int NC = D / 32;               // 16-byte pieces of 8 dims that a lane has of a row
-  constexpr int kStride = D * 2 + 64;      // bytes of a staged row (two rows: all 32 banks)
-  __shared__ __align__(16) uint8_t s_q[kKwRows * kStride];
-  __shared__ float s_lse[kKwRows];
+  constexpr int kStride = kKwStride<D>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint8_t* s_k = smem;                               // [128 keys][kStride]
+  uint8_t* s_q[2] = {smem + kKwKeys * kStride, smem + (kKwKeys + kKwRows) * kStride};
+  __shared__ __align__(8) float s_lse[2][kKwRows];
+  __shared__ float s_half[2][kKwKeys];     // sums of the two halves of the rows
+  __shared__ float s_sum[kKwKeys];         // of the CTA
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int quad = lane >> 2, qc = lane & 3;
+  const int group = warp & 3, half = warp >> 2;
+  const int rank = blockIdx.x % kKwCluster;
   const int total = a.chunk_start[a.num_seqs];
   const int G = a.num_q_heads / a.num_kv_heads;
+  // x / G for 0 <= x < 2^28 (G <= 16): the high word of x * ceil(2^32 / G) is off by less than
+  // x * 16 / 2^32 < 1 / G
+  const uint32_t magic = static_cast<uint32_t>(((1ull << 32) + G - 1) / G);
+  auto div_g = [&](int x) {
+    return G == 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), magic));
+  };
 
-  for (int64_t item = blockIdx.x; item < static_cast<int64_t>(total) * a.num_kv_heads;
-       item += gridDim.x) {
+  for (int64_t item = blockIdx.x / kKwCluster;
+       item < static_cast<int64_t>(total) * a.num_kv_heads; item += gridDim.x / kKwCluster) {
     const int chunk_id = static_cast<int>(item / a.num_kv_heads);
     const int h = static_cast<int>(item - static_cast<int64_t>(chunk_id) * a.num_kv_heads);
     int lo = 0, hi = a.num_seqs;  // largest s with chunk_start[s] <= chunk_id
@@ -169,125 +228,123 @@ __global__ void __launch_bounds__(kKwWarps * 32, 4) key_weights_kernel(const Key
     const int s = lo;
     const int t0 = a.qsl[s], n = a.qsl[s + 1] - t0, L = a.context_lens[s];
     const int base = (chunk_id - a.chunk_start[s]) * kKwKeys;  // first key of the item
-    const int key_w = base + 32 * warp;                         // first key of the warp
-
-    // ---- this lane's dims of its four keys as bf16 MMA fragments (A operand): keys
-    // key_w + 16 m + quad (+ 8); of piece c the dims 32 c + 8 qc .. + 7 --------------------
-    uint32_t kf[2][KS][4];
-    float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // [m][i]
-    bool there[2][2];  // keys of bad blocks, which the attention leaves out, receive nothing
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int key = key_w + 16 * m + quad + 8 * i;
-        int phys = -1;
-        if (key < L) {
-          phys = __ldg(a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq +
-                       key / kBlockSize);
-          if (phys >= a.num_blocks) phys = -1;  // (flagged by the attention)
-        }
-        there[m][i] = phys >= 0;
-        const int64_t tile = static_cast<int64_t>(phys) * a.num_kv_heads + h;
-        const int off = key % kBlockSize;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          uint32_t w[4] = {0u, 0u, 0u, 0u};  // 8 dims as bf16 pairs
-          if (phys >= 0) {
-            if constexpr (kPool == Pool::kBf16) {
-              const uint4 x = __ldg(reinterpret_cast<const uint4*>(
-                  a.k_cache + ((tile * kBlockSize + off) * D + 32 * c + 8 * qc) * 2));
-              w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-            } else if constexpr (kPool == Pool::kE4m3) {
-              const uint2 x = __ldg(reinterpret_cast<const uint2*>(
-                  a.k_cache + (tile * kBlockSize + off) * D + 32 * c + 8 * qc));
-              const uint32_t u[2] = {x.x, x.y};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float f0, f1;
-                e4m3x2_to_f32x2(static_cast<uint16_t>(u[j >> 1] >> (16 * (j & 1))), f0, f1);
-                w[j] = pack_bf16x2(f0, f1);
-              }
-            } else {
-              const uint8_t* t = a.k_cache + tile * Mx<D>::kTileBytes;
-              const uint16_t* src = reinterpret_cast<const uint16_t*>(t + off * Mx<D>::kRowBytes);
-              const uint32_t codes =
-                  __ldg(src + 2 * qc * NC + c) |
-                  (static_cast<uint32_t>(__ldg(src + (2 * qc + 1) * NC + c)) << 16);
-              const float sc = e8m0_to_f32(__ldg(t + Mx<D>::kCodeBytes + off * NC + c), 0);
-              uint32_t f[4];
-              e2m1x8_to_f16x2x4(codes, f);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&f[j]));
-                w[j] = pack_bf16x2(y.x * sc, y.y * sc);
-              }
-            }
-          }
-          // k-step 2 c: dims 0 1 (k = 2 qc) and 2 3 (k = 2 qc + 8); k-step 2 c + 1: 4 5 and 6 7
-          kf[m][2 * c][i] = w[0];
-          kf[m][2 * c][2 + i] = w[1];
-          kf[m][2 * c + 1][i] = w[2];
-          kf[m][2 * c + 1][2 + i] = w[3];
-        }
-      }
-
-    // ---- the rows of the tokens that see some key of the item -----------------------------
+    const int key_w = base + 32 * group;                        // first key of the warp
+    // the rows of the tokens that see some key of the item, in tiles of 64
     const int first_tok = max(0, base - (L - n));
     const int rows = (n - first_tok) * G;
-    for (int r0 = 0; r0 < rows; r0 += kKwRows) {
-      const int nr = min(kKwRows, rows - r0);
-      __syncthreads();  // the rows before are read
+    const int tiles = (rows + kKwRows - 1) / kKwRows;
+    auto stage = [&](int tile, int buf) {
+      const int r0 = tile * kKwRows, nr = min(kKwRows, rows - r0);
       for (int e = threadIdx.x; e < kKwRows * (D / 8); e += kKwWarps * 32) {
         const int r = e / (D / 8), c = e - r * (D / 8);
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (r < nr) {
-          const int tok = t0 + first_tok + (r0 + r) / G;
-          x = __ldg(reinterpret_cast<const uint4*>(
-              a.q + (static_cast<int64_t>(tok) * a.num_q_heads + h * G + (r0 + r) % G) * D + 8 * c));
-        }
-        *reinterpret_cast<uint4*>(s_q + r * kStride + 16 * c) = x;
+        const int at = r0 + min(r, nr - 1);  // (rows past the run: zeros)
+        const int tok = div_g(at);
+        cp_async16_zfill(
+            smem_u32(s_q[buf] + r * kStride + 16 * c),
+            a.q + (static_cast<int64_t>(t0 + first_tok + tok) * a.num_q_heads + h * G + at - tok * G) * D +
+                8 * c,
+            r < nr ? 16 : 0);
       }
-      for (int r = threadIdx.x; r < kKwRows; r += kKwWarps * 32)
-        s_lse[r] = r < nr ? a.lse[static_cast<int64_t>(t0 + first_tok + (r0 + r) / G) *
-                                      a.num_q_heads + h * G + (r0 + r) % G]
-                          : CUDART_INF_F;  // 2^(0 - inf) = 0
-      __syncthreads();
-      for (int rt = 0; rt < nr; rt += 8) {
+      if (threadIdx.x < kKwRows) {
+        const int r = threadIdx.x, at = r0 + r, tok = div_g(at);
+        if (r < nr)
+          cp_async4(smem_u32(&s_lse[buf][r]),
+                    a.lse + static_cast<int64_t>(t0 + first_tok + tok) * a.num_q_heads + h * G + at -
+                        tok * G);
+        else
+          s_lse[buf][r] = CUDART_INF_F;  // 2^(0 - inf) = 0
+      }
+      cp_async_commit();
+    };
+    // ---- the item's keys as bf16 in shared memory, then as MMA fragments (A operand): keys
+    // key_w + 16 m + quad (+ 8).  (Loaded straight into registers, a key's 16 bytes are four
+    // registers of two fragments, and moving them cost as much as the MMAs.) -----------------
+    if (rank < tiles) {
+      for (int e = threadIdx.x; e < kKwKeys * (D / 8); e += kKwWarps * 32) {
+        const int k = e / (D / 8), c = e - k * (D / 8), key = base + k;
+        int phys = -1;
+        if (key < L)
+          phys = __ldg(a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq +
+                       key / kBlockSize);
+        const bool ok = phys >= 0 && phys < a.num_blocks;
+        const int64_t tile = static_cast<int64_t>(ok ? phys : 0) * a.num_kv_heads + h;
+        uint8_t* dst = s_k + k * kStride + 16 * c;
+        if constexpr (kPool == Pool::kBf16) {
+          cp_async16_zfill(
+              smem_u32(dst),
+              a.k_cache + ((tile * kBlockSize + key % kBlockSize) * D + 8 * c) * 2, ok ? 16 : 0);
+        } else {
+          uint32_t w[4] = {0u, 0u, 0u, 0u};
+          if (ok) load_dims<kPool, D>(a.k_cache, tile, key % kBlockSize, c >> 2, c & 3, w);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      cp_async_commit();
+      stage(rank, 0);
+      cp_async_wait<1>();
+    }
+    __syncthreads();
+    uint32_t kf[2][KS][4];
+    float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // [m][i]
+    if (rank < tiles) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+          ldsm_x4(smem_u32(s_k + (32 * group + 16 * m + (lane & 15)) * kStride + 32 * ks +
+                           (lane >> 4) * 16),
+                  kf[m][ks][0], kf[m][ks][1], kf[m][ks][2], kf[m][ks][3]);
+    }
+
+    int buf = 0;
+    for (int tile = rank; tile < tiles; tile += kKwCluster, buf ^= 1) {
+      const int r0 = tile * kKwRows, nr = min(kKwRows, rows - r0);
+      cp_async_wait<0>();
+      __syncthreads();  // the tile is staged, and everyone is done with the buffer of the last one
+      if (tile + kKwCluster < tiles) stage(tile + kKwCluster, buf ^ 1);
+      for (int rt = 32 * half; rt < min(nr, 32 * half + 32); rt += 8) {
         float acc[2][4];
 #pragma unroll
-        for (int m = 0; m < 2; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const uint4 x = *reinterpret_cast<const uint4*>(s_q + (rt + quad) * kStride + 64 * c + 16 * qc);
+        for (int k2 = 0; k2 < KS / 2; ++k2) {  // two k-steps of the tile's eight rows
+          uint32_t b[4];
+          ldsm_x4(smem_u32(s_q[buf] + (rt + (lane & 7)) * kStride + 64 * k2 + (lane >> 3) * 16),
+                  b[0], b[1], b[2], b[3]);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            mma_bf16(acc[m], kf[m][2 * c], x.x, x.y);
-            mma_bf16(acc[m], kf[m][2 * c + 1], x.z, x.w);
+            if (k2 == 0) mma_bf16_zero(acc[m], kf[m][0], b[0], b[1]);
+            else mma_bf16(acc[m], kf[m][2 * k2], b[0], b[1]);
+            mma_bf16(acc[m], kf[m][2 * k2 + 1], b[2], b[3]);
           }
         }
-        // position of the tile's first row: rows that do not see a key add nothing to it
-        const int pos0 = L - n + first_tok + (r0 + rt) / G;
-        const bool all = key_w + 31 <= pos0;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float lse = s_lse[rt + 2 * qc + j];
-          const int pos = all ? INT_MAX
-                              : (rt + 2 * qc + j < nr
-                                     ? L - n + first_tok + (r0 + rt + 2 * qc + j) / G : -1);
+        const float2 lse = *reinterpret_cast<const float2*>(&s_lse[buf][rt + 2 * qc]);
+        // rows that do not see a key add nothing to it; every row sees the warp's keys if the
+        // tile's first does
+        if (key_w + 31 <= L - n + first_tok + div_g(r0 + rt)) {
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float w = fast_exp2(fmaf(acc[m][2 * i + j], a.score_log2, -lse));
-              if (key_w + 16 * m + quad + 8 * i <= pos) sum[m][i] += w;
+              sum[m][i] += fast_exp2(fmaf(acc[m][2 * i], a.score_log2, -lse.x));
+              sum[m][i] += fast_exp2(fmaf(acc[m][2 * i + 1], a.score_log2, -lse.y));
             }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r = rt + 2 * qc + j;
+            const int pos = r < nr ? L - n + first_tok + div_g(r0 + r) : -1;
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float w =
+                    fast_exp2(fmaf(acc[m][2 * i + j], a.score_log2, j ? -lse.y : -lse.x));
+                if (key_w + 16 * m + quad + 8 * i <= pos) sum[m][i] += w;
+              }
+          }
         }
       }
     }
-    // ---- sums over the four lanes of a key, and the update --------------------------------
-    const int64_t row = a.weight_rows ? a.weight_rows[s] : s;
-    float* W = a.key_weights + (row * a.num_kv_heads + h) * static_cast<int64_t>(a.max_keys);
+    // ---- sums over the four lanes of a key, the halves and the CTAs, and the update ---------
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -295,10 +352,30 @@ __global__ void __launch_bounds__(kKwWarps * 32, 4) key_weights_kernel(const Key
         float x = sum[m][i];
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
-        const int key = key_w + 16 * m + quad + 8 * i;
-        if (qc == 0 && key < L) W[key] = fmaf(a.decay, W[key], there[m][i] ? x : 0.f);
+        if (qc == 0) s_half[half][32 * group + 16 * m + quad + 8 * i] = x;
       }
     __syncthreads();
+    if (threadIdx.x < kKwKeys) s_sum[threadIdx.x] = s_half[0][threadIdx.x] + s_half[1][threadIdx.x];
+    cluster_arrive();
+    cluster_wait();  // every CTA's sums are there
+    constexpr int kShare = kKwKeys / kKwCluster;  // keys that this CTA updates
+    if (threadIdx.x < kShare) {
+      const int k = rank * kShare + threadIdx.x, key = base + k;
+      float x = 0.f;
+#pragma unroll
+      for (int c = 0; c < kKwCluster; ++c) x += ld_cluster(&s_sum[k], c);
+      if (key < L) {
+        const int phys = __ldg(a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq +
+                               key / kBlockSize);
+        // keys of bad blocks, which the attention leaves out, receive nothing
+        if (phys < 0 || phys >= a.num_blocks) x = 0.f;
+        const int64_t row = a.weight_rows ? a.weight_rows[s] : s;
+        float* W = a.key_weights + (row * a.num_kv_heads + h) * static_cast<int64_t>(a.max_keys);
+        W[key] = fmaf(a.decay, W[key], x);
+      }
+    }
+    cluster_arrive();
+    cluster_wait();  // the sums are read before they are written again
   }
 }
 
@@ -306,12 +383,14 @@ template <Pool kPool, int D>
 cudaError_t run_key_weights(const KeyWeightsArgs& a, cudaStream_t stream) {
   auto kern = key_weights_kernel<kPool, D>;
   LaunchInfo li;
-  cudaError_t e = launch_info(kern, kKwWarps * 32, 0, &li);
+  cudaError_t e = launch_info(kern, kKwWarps * 32, kKwSmem<D>, &li);
   if (e != cudaSuccess) return e;
   const int64_t upper = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads *
                         ((a.max_context_len + int64_t(kKwKeys) - 1) / kKwKeys);
-  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(upper, int64_t(li.sms) * li.per_sm));
-  return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kKwWarps * 32), 0, stream, a);
+  const int64_t resident = int64_t(li.sms) * li.per_sm / kKwCluster;
+  const int64_t clusters = std::max<int64_t>(1, std::min(upper, resident));
+  return launch_dependent(kern, dim3(static_cast<unsigned>(clusters * kKwCluster)),
+                          dim3(kKwWarps * 32), kKwSmem<D>, stream, a);
 }
 
 }  // namespace
