@@ -241,6 +241,7 @@ size_t pa_evict_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t m
  *   new_lens      [num_seqs] int32 (device): k.  It may not overlap context_lens, keep_lens or the
  *                 row tables.
  *   workspace     >= pa_evict_workspace_size(...) bytes (device).
+ * Built for the caches that pa_attention reads.
  * A sequence with a negative length, more keys than max_context_len or its table hold, a k above
  * max_keep_len (PA_DEVERR_LENGTHS), or a row past key_weights (PA_DEVERR_WEIGHT_ROW) or negative
  * (no error) is left as it is: its new_lens is its context length and its kept are -1.  A block

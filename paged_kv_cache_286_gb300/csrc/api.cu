@@ -691,7 +691,7 @@ pa_status pa_evict_keys(void* k_cache, void* v_cache, const pa_cache_desc* cache
   g_last_error.clear();
   if (num_seqs < 0 || max_keep_len < 0 || recent < 0)
     return fail(PA_ERR_INVALID_ARG, "negative size");
-  pa_status st = check_cache_desc(cache, false);
+  pa_status st = check_cache_desc(cache, true);
   if (st != PA_OK) return st;
   const bool nothing = num_seqs == 0;
   if (!nothing && max_context_len <= 0)

@@ -6,12 +6,13 @@
 // 0 .. k - 1; their weights move with them and the weights of positions k .. L - 1 become 0.
 //
 //  * select_kernel: one CTA per (sequence, kv head).  The weights are mapped to integers of the
-//    same order; three histogram passes of 11, 11 and 10 bits find the (k - r)-th largest and how
-//    many of its equals are kept; a last pass, in order, writes the kept positions and weights.
+//    same order, which stay in shared memory; three histogram passes of 11, 11 and 10 bits find
+//    the (k - r)-th largest and how many of its equals are kept; a last pass, in order, writes the
+//    kept positions and weights.
 //  * move_kernel: one CTA per (sequence, kv head, K or V, column slice).  A kept key never moves
 //    up, so rows can move in place if a batch of them is read before it is written and batches go
-//    in order: every source of a later batch lies above all that is written so far.  Batch c + 1
-//    is loaded into registers before batch c is stored, so loads are always in flight.
+//    in order: every source of a later batch lies above all that is written so far.  The rows of
+//    the next batch are looked up while a batch's loads are in flight.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -23,10 +24,6 @@
 namespace pa {
 
 namespace {
-
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelPer = 4;  // positions of a lane in a pass of the CTA
 
 struct EvictSeq {
   int L, k, r, row, dst_row;
@@ -64,9 +61,33 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) {
+constexpr int kSelPer = 8;  // positions of a lane in a round of the last pass
+
+// Exclusive sum over the CTA's warps of each warp's `mine` (the same in all its lanes), through
+// `slots`; *all is the total.  A barrier before it is the caller's.
+template <int kWarps>
+__device__ __forceinline__ int warps_exclusive(int mine, int* slots, int* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) slots[warp] = mine;
+  __syncthreads();
+  int x = lane < kWarps ? slots[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  *all = __shfl_sync(0xffffffffu, x, kWarps - 1);
+  return __shfl_sync(0xffffffffu, x, warp) - mine;
+}
+
+// `cached`: the order keys of that many first positions stay in shared memory between the passes.
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a, int cached) {
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kBins = 2048 / kThreads;  // of a thread
+  extern __shared__ uint32_t s_key[];
   __shared__ int hist[2048];
-  __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps];
+  __shared__ int slots[2][kWarps];
   __shared__ int s_digit, s_above;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -79,7 +100,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
     a.new_lens[s] = e.ok ? e.k : e.L;
   }
   int32_t* kept = a.kept + (static_cast<int64_t>(s) * a.num_kv_heads + h) * a.max_keep_len;
-  for (int i = e.k + tid; i < a.max_keep_len; i += kSelThreads) kept[i] = -1;
+  for (int i = e.k + tid; i < a.max_keep_len; i += kThreads) kept[i] = -1;
   if (!e.ok) return;
   const float* W = a.key_weights +
                    (static_cast<int64_t>(e.row) * a.num_kv_heads + h) * a.max_keys;
@@ -94,20 +115,29 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const int nbits = pass == 2 ? 10 : 11;
-      for (int i = tid; i < 2048; i += kSelThreads) hist[i] = 0;
+      for (int i = tid; i < 2048; i += kThreads) hist[i] = 0;
       __syncthreads();
-      for (int j = tid; j < N; j += kSelThreads) {
-        const uint32_t u = order_key(W[j]);
-        if (pass == 0 || (u >> (shift + nbits)) == prefix)
-          atomicAdd(&hist[(u >> shift) & ((1u << nbits) - 1)], 1);
+      if (pass == 0) {
+#pragma unroll 4
+        for (int j = tid; j < N; j += kThreads) {
+          const uint32_t u = order_key(W[j]);
+          if (j < cached) s_key[j] = u;
+          atomicAdd(&hist[u >> 21], 1);
+        }
+      } else {
+#pragma unroll 4
+        for (int j = tid; j < N; j += kThreads) {
+          const uint32_t u = j < cached ? s_key[j] : order_key(W[j]);
+          if ((u >> (shift + nbits)) == prefix) atomicAdd(&hist[(u >> shift) & ((1u << nbits) - 1)], 1);
+        }
       }
       __syncthreads();
-      // the digit at which the count from the top reaches `need`: thread t sums four bins from
+      // the digit at which the count from the top reaches `need`: a thread sums kBins bins from
       // the top, then a scan over the CTA
-      int c[4], sum = 0;
+      int c[kBins], sum = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[i] = hist[2047 - (4 * tid + i)];
+      for (int i = 0; i < kBins; ++i) {
+        c[i] = hist[2047 - (kBins * tid + i)];
         sum += c[i];
       }
       int x = sum;
@@ -116,14 +146,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
-      if (lane == 31) warp_gt[warp] = x;
-      __syncthreads();
-      int before = x - sum;
-      for (int w = 0; w < warp; ++w) before += warp_gt[w];
+      int all;
+      int before = warps_exclusive<kWarps>(__shfl_sync(0xffffffffu, x, 31), slots[pass & 1], &all) +
+                   x - sum;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kBins; ++i) {
         if (before < need && need <= before + c[i]) {
-          s_digit = 2047 - (4 * tid + i);
+          s_digit = 2047 - (kBins * tid + i);
           s_above = before;
         }
         before += c[i];
@@ -131,55 +160,46 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
       __syncthreads();
       prefix = (prefix << nbits) | static_cast<uint32_t>(s_digit);
       need -= s_above;
-      __syncthreads();
     }
   }
   // kept: order key above `prefix`, the first `need` equal to it, and the last r
-  const bool none = m == 0, all = m == N;
+  const bool none = m == 0, all_stay = m == N;
   int done = 0, done_eq = 0;  // kept so far; equals so far
-  for (int base = 0; base < e.L; base += kSelThreads * kSelPer) {
+  for (int base = 0; base < e.L; base += kThreads * kSelPer) {
     float w[kSelPer];
     unsigned gt[kSelPer], eq[kSelPer];
     int n_gt = 0, n_eq = 0;
+    const int first = base + warp * (32 * kSelPer) + lane;
+#pragma unroll
+    for (int i = 0; i < kSelPer; ++i) w[i] = first + 32 * i < e.L ? W[first + 32 * i] : 0.f;
 #pragma unroll
     for (int i = 0; i < kSelPer; ++i) {
-      const int j = base + warp * (32 * kSelPer) + 32 * i + lane;
-      w[i] = j < e.L ? W[j] : 0.f;
+      const int j = first + 32 * i;
       const uint32_t u = order_key(w[i]);
       const bool in = j < N;
-      const bool g = j < e.L && (!in || all || (!none && u > prefix));
+      const bool g = j < e.L && (!in || all_stay || (!none && u > prefix));
       gt[i] = __ballot_sync(0xffffffffu, g);
-      eq[i] = __ballot_sync(0xffffffffu, in && !all && !none && u == prefix);
+      eq[i] = __ballot_sync(0xffffffffu, in && !all_stay && !none && u == prefix);
       n_gt += __popc(gt[i]);
       n_eq += __popc(eq[i]);
     }
-    if (lane == 0) {
-      warp_gt[warp] = n_gt;
-      warp_eq[warp] = n_eq;
-    }
-    __syncthreads();  // (and every weight of this pass is read before one is written)
-    int b_gt = 0, b_eq = done_eq, t_gt = 0, t_eq = 0;
-    for (int v = 0; v < kSelWarps; ++v) {
-      if (v < warp) {
-        b_gt += warp_gt[v];
-        b_eq += warp_eq[v];
-      }
-      t_gt += warp_gt[v];
-      t_eq += warp_eq[v];
-    }
+    int t_gt, t_eq;
+    __syncthreads();  // (the slots' readers of the round before are done)
+    // (the barriers in these: every weight of the round is read before one is written)
+    int b_gt = warps_exclusive<kWarps>(n_gt, slots[0], &t_gt);
+    int b_eq = warps_exclusive<kWarps>(n_eq, slots[1], &t_eq) + done_eq;
     // place of a kept key: those kept before it, done + (above since `base`) + (equals kept
     // since `base`)
     const int eq_kept0 = min(done_eq, need);
+    const unsigned below = (1u << lane) - 1;
 #pragma unroll
     for (int i = 0; i < kSelPer; ++i) {
-      const int j = base + warp * (32 * kSelPer) + 32 * i + lane;
-      const unsigned below = (1u << lane) - 1;
       const int rank_eq = b_eq + __popc(eq[i] & below);
       const bool is_eq = (eq[i] >> lane) & 1;
       const bool keep = ((gt[i] >> lane) & 1) || (is_eq && rank_eq < need);
       const int at = done + b_gt + __popc(gt[i] & below) + min(rank_eq, need) - eq_kept0;
       if (keep) {
-        kept[at] = j;
+        kept[at] = first + 32 * i;
         Wd[at] = w[i];
       }
       b_gt += __popc(gt[i]);
@@ -187,19 +207,19 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
     }
     done += t_gt + min(done_eq + t_eq, need) - eq_kept0;
     done_eq += t_eq;
-    __syncthreads();
   }
-  for (int i = e.k + tid; i < e.L; i += kSelThreads) Wd[i] = 0.f;
+  __syncthreads();  // every weight is read
+  for (int i = e.k + tid; i < e.L; i += kThreads) Wd[i] = 0.f;
 }
 
 constexpr int kMoveThreads = 256;
 constexpr int kMovePer = 4;  // 16-byte pieces of a thread in a batch
 
-// kVec: 16-byte pieces of a row's slice.  MXFP4 rows (kNB > 0) also have kNB scale bytes, which
-// the threads with the row's first piece move.
+// vec: 16-byte pieces of a row's slice.  MXFP4 rows (kNB > 0) also have kNB scale bytes, which the
+// threads with the row's first piece move.
 template <int kNB>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, int row_bytes,
-                                                            int slices, int vec) {
+                                                            int slices, int vec_log2) {
   grid_dependency_wait();
   int id = blockIdx.x;
   const int slice = id % slices;
@@ -214,64 +234,82 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
   const int32_t* kept = a.kept + (static_cast<int64_t>(s) * a.num_kv_heads + h) * a.max_keep_len;
   const int32_t* src_t = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
   const int32_t* dst_t = a.dst_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
-  const int tile_bytes = row_bytes * kBlockSize + kNB * kBlockSize;
-  const int rows = kMoveThreads * kMovePer / vec;  // rows of a batch
-  uint4 x[2][kMovePer];
-  uint32_t sc[2][kMovePer];
-  int64_t to[2][kMovePer];  // byte offset of the destination row, or -1
-  auto load = [&](int buf, int first) {
+  const int vec = 1 << vec_log2;
+  const int rows = (kMoveThreads * kMovePer) >> vec_log2;  // rows of a batch
+  const int c = threadIdx.x & (vec - 1);                   // this thread's piece of its rows
+  const int col = (slice * vec + c) * 16;
+  const int my_row = threadIdx.x >> vec_log2, row_step = kMoveThreads >> vec_log2;
+  // a row of the pool ((block, kv head) tile x slot) as a byte offset
+  auto offset = [&](int32_t row) {
+    if constexpr (kNB == 0) return static_cast<int64_t>(row) * row_bytes;
+    return static_cast<int64_t>(row >> 4) * (kBlockSize * (row_bytes + kNB)) + (row & 15) * row_bytes;
+  };
+  auto scales = [&](int32_t row) {
+    return pool + static_cast<int64_t>(row >> 4) * (kBlockSize * (row_bytes + kNB)) +
+           kBlockSize * row_bytes + (row & 15) * kNB;
+  };
+  int32_t from[2][kMovePer], to[2][kMovePer];  // pool rows (fewer than 2^31) of a batch; -1: none
+  uint4 x[kMovePer];
+  uint32_t sc[kMovePer];
+  auto find = [&](int buf, int first) {
 #pragma unroll
     for (int i = 0; i < kMovePer; ++i) {
-      const int unit = i * kMoveThreads + threadIdx.x;
-      const int r = unit / vec, c = unit - r * vec;
-      const int at = first + r;
-      to[buf][i] = -1;
-      if (at < e.k && r < rows) {
+      const int at = first + my_row + i * row_step;
+      from[buf][i] = to[buf][i] = -1;
+      if (at < e.k) {
         const int j = kept[at];
         const int from_b = __ldg(src_t + j / kBlockSize), to_b = __ldg(dst_t + at / kBlockSize);
         if (from_b < 0 || from_b >= a.num_blocks || to_b < 0 || to_b >= a.num_blocks) {
           set_error(a.err, PA_DEVERR_BLOCK_ID);
         } else if (from_b != to_b || j % kBlockSize != at % kBlockSize) {
-          const int64_t ft = (static_cast<int64_t>(from_b) * a.num_kv_heads + h) * tile_bytes;
-          const int64_t tt = (static_cast<int64_t>(to_b) * a.num_kv_heads + h) * tile_bytes;
-          const int fo = j % kBlockSize, tof = at % kBlockSize;
-          const int col = (slice * vec + c) * 16;
-          x[buf][i] = *reinterpret_cast<const uint4*>(pool + ft + fo * row_bytes + col);
-          to[buf][i] = tt + tof * row_bytes + col;
-          if (kNB == 4 && col == 0)
-            sc[buf][i] = *reinterpret_cast<const uint32_t*>(pool + ft + kBlockSize * row_bytes + fo * kNB);
-          if (kNB == 2 && col == 0)
-            sc[buf][i] = *reinterpret_cast<const uint16_t*>(pool + ft + kBlockSize * row_bytes + fo * kNB);
+          from[buf][i] = (from_b * a.num_kv_heads + h) * kBlockSize + j % kBlockSize;
+          to[buf][i] = (to_b * a.num_kv_heads + h) * kBlockSize + at % kBlockSize;
         }
       }
+    }
+  };
+  auto load = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kMovePer; ++i) {
+      if (from[buf][i] < 0) continue;
+      x[i] = *reinterpret_cast<const uint4*>(pool + offset(from[buf][i]) + col);
+      if (kNB == 4 && col == 0) sc[i] = *reinterpret_cast<const uint32_t*>(scales(from[buf][i]));
+      if (kNB == 2 && col == 0) sc[i] = *reinterpret_cast<const uint16_t*>(scales(from[buf][i]));
     }
   };
   auto store = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < kMovePer; ++i) {
       if (to[buf][i] < 0) continue;
-      *reinterpret_cast<uint4*>(pool + to[buf][i]) = x[buf][i];
-      if (kNB > 0) {
-        const int unit = i * kMoveThreads + threadIdx.x;
-        if (slice == 0 && unit % vec == 0) {
-          const int64_t tile = to[buf][i] / tile_bytes * tile_bytes;
-          const int off = static_cast<int>(to[buf][i] - tile) / row_bytes;
-          uint8_t* d = pool + tile + kBlockSize * row_bytes + off * kNB;
-          if (kNB == 4) *reinterpret_cast<uint32_t*>(d) = sc[buf][i];
-          else *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(sc[buf][i]);
-        }
-      }
+      *reinterpret_cast<uint4*>(pool + offset(to[buf][i]) + col) = x[i];
+      if (kNB == 4 && col == 0) *reinterpret_cast<uint32_t*>(scales(to[buf][i])) = sc[i];
+      if (kNB == 2 && col == 0)
+        *reinterpret_cast<uint16_t*>(scales(to[buf][i])) = static_cast<uint16_t>(sc[i]);
     }
   };
-  load(0, 0);
+  find(0, 0);
   for (int first = 0; first < e.k; first += 2 * rows) {
-    load(1, first + rows);
-    __syncthreads();  // batch 0 of this round is read by everyone
+    // a batch is loaded, the next one's rows are found, and once everyone has loaded it is stored
+    load(0);
+    find(1, first + rows);
+    __syncthreads();
     store(0);
-    load(0, first + 2 * rows);
+    load(1);
+    find(0, first + 2 * rows);
     __syncthreads();
     store(1);
   }
+}
+
+template <int kThreads>
+cudaError_t run_select(const EvictArgs& a, int64_t pairs, cudaStream_t stream) {
+  // order keys of as many positions as shared memory holds
+  const int cached = std::min(a.max_context_len, 50 * 1024);
+  LaunchInfo li;
+  cudaError_t e = launch_info(select_kernel<kThreads>, kThreads, 50 * 1024 * 4, &li);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(select_kernel<kThreads>, dim3(static_cast<unsigned>(pairs)),
+                          dim3(kThreads), cached * 4, stream, a, cached);
 }
 
 }  // namespace
@@ -280,16 +318,26 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   const int row_bytes = a.cache_dtype == PA_MXFP4 ? a.head_dim / 2
                         : a.cache_dtype == PA_FP8_E4M3 ? a.head_dim : 2 * a.head_dim;
-  const int vecs = row_bytes / 16;
   const int64_t ctas = 2 * pairs;
-  if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-  cudaError_t e = launch_dependent(select_kernel, dim3(static_cast<unsigned>(pairs)),
-                                   dim3(kSelThreads), 0, stream, a);
+  if (4 * ctas > INT32_MAX) return cudaErrorInvalidValue;
+  cudaError_t e = a.max_context_len <= 8192 ? run_select<512>(a, pairs, stream)
+                                            : run_select<1024>(a, pairs, stream);
   if (e != cudaSuccess || a.max_keep_len == 0) return e;
+  // Batches of a (sequence, kv head, K or V) go one after another, but columns are independent:
+  // few of them are cut into slices of at least 64 bytes until they fill the GPU.
+  int dev = 0, sms = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  int slices = 1, vec_log2 = 0;
+  while ((16 << vec_log2) < row_bytes) ++vec_log2;
+  while (ctas * slices < 8 * int64_t(sms) && vec_log2 > 2) {
+    slices *= 2;
+    --vec_log2;
+  }
   auto kern = a.cache_dtype != PA_MXFP4 ? move_kernel<0>
               : a.head_dim == 128       ? move_kernel<4> : move_kernel<2>;
-  return launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), dim3(kMoveThreads), 0, stream,
-                          a, row_bytes, 1, vecs);
+  return launch_dependent(kern, dim3(static_cast<unsigned>(ctas * slices)), dim3(kMoveThreads), 0,
+                          stream, a, row_bytes, slices, vec_log2);
 }
 
 }  // namespace pa

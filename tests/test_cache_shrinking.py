@@ -174,6 +174,7 @@ def _evict(lib, **kw):
     (dict(dst=at(0x100002)), 1), (dict(drows=at(0x100001)), 1), (dict(ws=None), 1), (dict(wsb=100), 1),
     (dict(lens=at(0x200000)), 1), (dict(lens=at(0x20000c)), 1), (dict(lens=at(0x210000)), 1),
     (dict(rows=at(0x220008)), 1), (dict(desc=_desc(head_dim=72, cache_dtype=0)), 2),
+    (dict(desc=_desc(head_dim=80, cache_dtype=0)), 2), (dict(desc=_desc(head_dim=64, cache_dtype=1)), 2),
 ])
 def test_evict_refusals(lib, kw, status):
     assert _evict(lib, **kw) == status
