@@ -89,8 +89,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a, int
   __shared__ int hist[2048];
   __shared__ int slots[2][kWarps];
   __shared__ int s_digit, s_above;
-  grid_dependency_wait();
-  grid_launch_dependents();
+  grid_dependency_wait();  // (the moves are not launched early: their CTAs would take SMs from this)
   const int s = blockIdx.x / a.num_kv_heads, h = blockIdx.x - s * a.num_kv_heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t bits;
@@ -320,17 +319,21 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
                         : a.cache_dtype == PA_FP8_E4M3 ? a.head_dim : 2 * a.head_dim;
   const int64_t ctas = 2 * pairs;
   if (4 * ctas > INT32_MAX) return cudaErrorInvalidValue;
-  cudaError_t e = a.max_context_len <= 8192 ? run_select<512>(a, pairs, stream)
-                                            : run_select<1024>(a, pairs, stream);
-  if (e != cudaSuccess || a.max_keep_len == 0) return e;
-  // Batches of a (sequence, kv head, K or V) go one after another, but columns are independent:
-  // few of them are cut into slices of at least 64 bytes until they fill the GPU.
   int dev = 0, sms = 0;
+  cudaError_t e;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  // A pass over short rows costs mostly what every warp does once (bins, scans), so few warps a CTA
+  // and many CTAs; long rows, or few, want the CTA's time short.
+  e = a.max_context_len <= 4096 || pairs >= 8 * int64_t(sms) ? run_select<128>(a, pairs, stream)
+      : a.max_context_len <= 8192                            ? run_select<512>(a, pairs, stream)
+                                                             : run_select<1024>(a, pairs, stream);
+  if (e != cudaSuccess || a.max_keep_len == 0) return e;
+  // Batches of a (sequence, kv head, K or V) go one after another, but columns are independent:
+  // few of them are cut into slices of at least 64 bytes, while they all are resident at once.
   int slices = 1, vec_log2 = 0;
   while ((16 << vec_log2) < row_bytes) ++vec_log2;
-  while (ctas * slices < 8 * int64_t(sms) && vec_log2 > 2) {
+  while (ctas * slices * 2 <= 4 * int64_t(sms) && vec_log2 > 2) {
     slices *= 2;
     --vec_log2;
   }
