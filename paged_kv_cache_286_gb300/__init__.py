@@ -22,6 +22,7 @@ eviction of the keys that received the least attention:
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
@@ -46,19 +47,24 @@ def version() -> str:
     return _lib.load().pa_version().decode()
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+def _ptr(t: Optional[torch.Tensor]) -> int:
+    return t.data_ptr() if t is not None else 0
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream) -> int:
+    """The stream's handle (None: the current device's current stream)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _need(t: torch.Tensor, name: str, dtypes, ndim: int):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == ndim and \
+            t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
@@ -165,9 +171,9 @@ def _step_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
     _need(query_start_loc, "query_start_loc", (torch.int32,), 1)
     _need(workspace, "workspace", (torch.uint8,), 1)
     T, Hq, D = q.shape
-    S = context_lens.shape[0]
-    Hkv = k_cache.shape[1]
-    if query_start_loc.shape[0] != S + 1 or block_tables.shape[0] != S:
+    S = context_lens.size(0)
+    Hkv = k_cache.size(1)
+    if query_start_loc.size(0) != S + 1 or block_tables.size(0) != S:
         raise ValueError("query_start_loc must have num_seqs + 1 entries and block_tables "
                          "num_seqs rows")
     if out is None:
@@ -180,33 +186,36 @@ def _step_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
     desc = cache_desc(k_cache, k_scale, v_scale)
     return out, (
         _ptr(q), T, _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc), _ptr(block_tables),
-        block_tables.shape[1], _ptr(context_lens), _ptr(query_start_loc), S,
+        block_tables.size(1), _ptr(context_lens), _ptr(query_start_loc), S,
         int(max_context_len), int(max_query_len), Hq, Hkv, D, float(scale), _ptr(out), odt)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _on(stream, *tensors):
     """Checks that the tensors (None: absent) share one device and returns a context in which the
     call's allocations and its launch are on that device and on `stream` (None: the device's
     current stream)."""
-    dev = tensors[0].device
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {t.device} and {dev}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {t.device} and {tensors[0].device}")
     if stream is None:
-        return torch.cuda.device(dev)
-    if stream.device != dev:
-        raise ValueError(f"stream of {stream.device} for tensors on {dev}")
+        return _HERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream of {stream.device} for tensors on {tensors[0].device}")
     return torch.cuda.stream(stream)
 
 
 def _need_weights(key_weights, num_kv_heads, num_seqs, **rows):
     _need(key_weights, "key_weights", (torch.float32,), 3)
-    if key_weights.shape[1] != num_kv_heads:
+    if key_weights.size(1) != num_kv_heads:
         raise ValueError("key_weights must be [rows, num_kv_heads, max_keys]")
     for name, r in rows.items():
         if r is not None:
             _need(r, name, (torch.int32,), 1)
-            if r.shape[0] != num_seqs:
+            if r.size(0) != num_seqs:
                 raise ValueError(f"{name} must have num_seqs entries")
 
 
@@ -233,15 +242,15 @@ def attention_key_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     _need_caches(k_cache, v_cache)
     _same_shape(k_cache, v_cache)
     _need(context_lens, "context_lens", (torch.int32,), 1)
-    _need_weights(key_weights, k_cache.shape[1], context_lens.shape[0], weight_rows=weight_rows)
+    _need_weights(key_weights, k_cache.size(1), context_lens.size(0), weight_rows=weight_rows)
     with _on(stream, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, key_weights,
              workspace, weight_rows, out):
         out, args = _step_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
                                workspace, scale, max_context_len, max_query_len, out, out_dtype,
                                k_scale, v_scale)
         _lib.check(_lib.load().pa_attention_key_weights(
-            *args, _ptr(key_weights), _ptr(weight_rows), key_weights.shape[0],
-            key_weights.shape[2], float(decay), _ptr(workspace), workspace.numel(),
+            *args, _ptr(key_weights), _ptr(weight_rows), key_weights.size(0),
+            key_weights.size(2), float(decay), _ptr(workspace), workspace.numel(),
             _stream(stream)))
     return out
 
@@ -270,9 +279,9 @@ def evict_keys(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch
     _need(context_lens, "context_lens", (torch.int32,), 1)
     _need(keep_lens, "keep_lens", (torch.int32,), 1)
     _need(workspace, "workspace", (torch.uint8,), 1)
-    S, H = context_lens.shape[0], k_cache.shape[1]
+    S, H = context_lens.size(0), k_cache.size(1)
     _need_weights(key_weights, H, S, weight_rows=weight_rows, dst_weight_rows=dst_weight_rows)
-    if block_tables.shape[0] != S or keep_lens.shape[0] != S:
+    if block_tables.size(0) != S or keep_lens.size(0) != S:
         raise ValueError("block_tables and keep_lens must have num_seqs rows")
     if dst_tables is not None:
         _need(dst_tables, "dst_tables", (torch.int32,), 2)
@@ -297,9 +306,9 @@ def evict_keys(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch
         desc = cache_desc(k_cache)
         _lib.check(_lib.load().pa_evict_keys(
             _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc), _ptr(block_tables),
-            _ptr(dst_tables), block_tables.shape[1], _ptr(context_lens), _ptr(keep_lens), S,
+            _ptr(dst_tables), block_tables.size(1), _ptr(context_lens), _ptr(keep_lens), S,
             int(max_context_len), int(max_keep_len), int(recent), _ptr(key_weights),
-            _ptr(weight_rows), _ptr(dst_weight_rows), key_weights.shape[0], key_weights.shape[2],
+            _ptr(weight_rows), _ptr(dst_weight_rows), key_weights.size(0), key_weights.size(2),
             _ptr(kept), _ptr(new_lens), _ptr(workspace), workspace.numel(), _stream(stream)))
     return kept, new_lens
 
@@ -353,7 +362,7 @@ def set_kernel_span_buffer(buf: Optional[torch.Tensor]) -> None:
         _need(buf, "span buffer", (torch.int64,), 1)
         if buf.numel() < 4:
             raise ValueError("the span buffer needs four entries")
-    _lib.load().pa_set_kernel_span_buffer(_ptr(buf) if buf is not None else ctypes.c_void_p(0))
+    _lib.load().pa_set_kernel_span_buffer(_ptr(buf))
 
 
 def set_prefill_timing_events(before: Optional[torch.cuda.Event],
