@@ -39,15 +39,18 @@ __device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t w, uint32_t (&out)[4]
       : "r"(w));
 }
 
-// Two fp32 to E2M1, round to nearest even, saturating at 6: `lo` -> low nibble.
-__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+// Eight fp32 to E2M1 codes, round to nearest even, saturating at 6: x[0] in the lowest nibble.
+__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&x)[8]) {
   uint32_t out;
-  asm("{\n\t.reg .b8 t;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
-      "mov.b32 %0, {t, 0, 0, 0};\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(out)
-      : "f"(hi), "f"(lo));
-  return out & 0xffu;
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return out;
 }
 
 // Scale byte `i` of a word as fp32.  Byte 0 gives 0 instead of 2^-127 (what it scales is below
