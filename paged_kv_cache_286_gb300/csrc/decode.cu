@@ -419,6 +419,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, NST == 2 ? 3 : 1)
     }
     const int my_head = HPI > 1 ? quad / p.group : 0;  // head of the item this lane's row uses
     float* score_row[RT];  // where this lane's rows' scores go, or NULL
+    uint64_t keep_scores = 0;  // they are read back soon: kept in L2 before the stream of K and V
+    if constexpr (kScores) keep_scores = policy_evict_last();
     if constexpr (kScores) {
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
@@ -630,8 +632,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, NST == 2 ? 3 : 1)
             if (score_row[r]) {
 #pragma unroll
               for (int nt = 0; nt < 2; ++nt)
-                *reinterpret_cast<float2*>(score_row[r] + key0 + 8 * nt + 2 * qc) =
-                    make_float2(sv[2 * nt], sv[2 * nt + 1]);
+                st_f32x2_hint(score_row[r] + key0 + 8 * nt + 2 * qc, sv[2 * nt], sv[2 * nt + 1],
+                              keep_scores);
             }
           }
           float mloc = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));

@@ -65,46 +65,64 @@ __device__ __forceinline__ int kw_chunks(const KeyWeightsArgs& a, int s, uint32_
 // keys, four neighbouring keys (of one block) to a thread.  Bound by the scores' bytes (mostly
 // L2's) and by launch.
 constexpr int kFinThreads = 256;
-constexpr int kFinShare = 2048;  // keys of a share at least (of the longest sequence)
+constexpr int kFinShare = 4096;  // keys of a share at least (of the longest sequence)
 __global__ void __launch_bounds__(kFinThreads) kw_finish_kernel(const KeyWeightsArgs a) {
   __shared__ float s_lse[kDecodeMaxRows];
   grid_dependency_wait();
-  const int s = blockIdx.x / a.num_kv_heads, h = blockIdx.x - s * a.num_kv_heads;
+  const int s = blockIdx.x, h = blockIdx.y;
   uint32_t bits = 0;
   const bool ok = kw_accumulates(a, s, &bits);
   if (bits && threadIdx.x == 0) set_error(a.err, bits);
   if (!ok) return;
   const int t0 = a.qsl[s], n = a.qsl[s + 1] - t0, L = a.context_lens[s];
   const int G = a.num_q_heads / a.num_kv_heads;
-  if (n * G > a.score_rows || (blockIdx.y && blockIdx.y * kFinShare >= L)) return;
-  if (threadIdx.x < n * G)
+  if (n * G > a.score_rows || (blockIdx.z && blockIdx.z * kFinShare >= L)) return;
+  const int rows = n * G;
+  if (threadIdx.x < rows)
     s_lse[threadIdx.x] = a.lse[static_cast<int64_t>(t0 + threadIdx.x / G) * a.num_q_heads + h * G +
                                threadIdx.x % G];
-  __syncthreads();
   const int row = a.weight_rows ? a.weight_rows[s] : s;
   float* W = a.key_weights + (static_cast<int64_t>(row) * a.num_kv_heads + h) * a.max_keys;
   const float* sc = a.scores + (static_cast<int64_t>(s) * a.num_kv_heads + h) * a.score_rows *
                                    a.score_stride;
   const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks_per_seq;
   const int groups = (L + 3) / 4;
-  const int share = max(kFinShare / 4, static_cast<int>((groups + gridDim.y - 1) / gridDim.y));
-  const int end = min(groups, share * (static_cast<int>(blockIdx.y) + 1));
-  for (int g = share * blockIdx.y + threadIdx.x; g < end; g += kFinThreads) {
-    const int key = 4 * g;
+  const int share = gridDim.z == 1 ? groups
+                                   : max(kFinShare / 4, static_cast<int>((groups + gridDim.z - 1) / gridDim.z));
+  const int end = min(groups, share * (static_cast<int>(blockIdx.z) + 1));
+  // rounds of the CTA; a round's loads (up to four rows of scores) go out together, the first
+  // round's before the log-sum-exps are there
+  for (int first = share * blockIdx.z; first < end; first += kFinThreads) {
+    const int g = first + threadIdx.x, key = 4 * g;
+    const bool mine = g < end;
     float w[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
+    float4 x[4];
+    int phys = -1;
+    const float* col = sc + key;
+    if (mine) {
+      phys = __ldg(table + key / kBlockSize);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = key + i < L ? W[key + i] : 0.f;
-    const int phys = __ldg(table + key / kBlockSize);
+      for (int i = 0; i < 4; ++i) w[i] = key + i < L ? W[key + i] : 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r < rows) x[r] = *reinterpret_cast<const float4*>(col + static_cast<int64_t>(r) * a.score_stride);
+    }
+    if (first == share * static_cast<int>(blockIdx.z)) __syncthreads();
+    if (!mine) break;
     if (phys >= 0 && phys < a.num_blocks) {  // (the attention leaves bad blocks out)
-      const float* col = sc + key;
-#pragma unroll 4
-      for (int r = 0; r < n * G; ++r) {
-        const float4 x = *reinterpret_cast<const float4*>(col + static_cast<int64_t>(r) * a.score_stride);
-        const int pos = L - n + r / G;  // the row's position: it sees keys up to this one
-        const float v[4] = {x.x, x.y, x.z, x.w};
+      for (int r0 = 0; r0 < rows; r0 += 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (key + i <= pos) sum[i] += fast_exp2(v[i] - s_lse[r]);
+        for (int r = 0; r < 4; ++r) {
+          if (r0 + r >= rows) break;
+          // the row's position: it sees keys up to this one
+          const int pos = n == 1 ? L - 1 : L - n + (r0 + r) / G;
+          const float v[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (key + i <= pos) sum[i] += fast_exp2(v[i] - s_lse[r0 + r]);
+          if (r0 + 4 + r < rows)
+            x[r] = *reinterpret_cast<const float4*>(col + static_cast<int64_t>(r0 + 4 + r) * a.score_stride);
+        }
       }
     }
 #pragma unroll
@@ -399,9 +417,9 @@ cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (a.scores) {
     const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
-    const int64_t shares = std::min<int64_t>((a.max_context_len + int64_t(kFinShare) - 1) / kFinShare, 64);
-    if (pairs > INT32_MAX) return cudaErrorInvalidValue;
-    e = launch_dependent(kw_finish_kernel, dim3(static_cast<unsigned>(pairs), unsigned(shares)),
+    const int64_t shares = std::min<int64_t>((a.max_context_len + int64_t(kFinShare) - 1) / kFinShare, 65535);
+    if (pairs > INT32_MAX || a.num_kv_heads > 65535) return cudaErrorInvalidValue;
+    e = launch_dependent(kw_finish_kernel, dim3(a.num_seqs, a.num_kv_heads, unsigned(shares)),
                          dim3(kFinThreads), 0, stream, a);
     if (e != cudaSuccess) return e;
   }
