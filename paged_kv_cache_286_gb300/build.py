@@ -20,7 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedattn.so")
 SOURCES = ["api.cu", "append.cu", "decode.cu", "decode_mx.cu", "mx_stage.cu", "noalloc.cu", "prefill.cu",
-           "copy.cu", "selftest.cu", "key_weights.cu", "evict.cu", "block_manager.cpp"]
+           "copy.cu", "selftest.cu", "key_weights.cu", "key_weights_tc.cu",
+           "evict.cu", "block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

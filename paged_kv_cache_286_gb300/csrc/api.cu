@@ -665,7 +665,29 @@ pa_status pa_attention_key_weights(
   a.score_log2 =
       scale * 1.4426950408889634f * (cache->cache_dtype == PA_FP8_E4M3 ? cache->k_scale : 1.f);
   a.decay = decay;
-  const cudaError_t e = pa::launch_key_weights(a, stream);
+  a.wait_ns = g_wait_ns;
+  a.skip_copy = g_skip_copy;
+  // Long runs over bf16 keys go to the tensor-core kernel if their key chunks, one to a CTA, fill at
+  // least half the SMs; with fewer, four CTAs to a chunk of the other kernel end sooner.
+  pa::PoolMaps maps;
+  bool tc = a.k_pass && cache->cache_dtype == PA_BF16 &&
+            pa::prefill_geometry(num_q_heads, num_kv_heads);
+  if (tc) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_fail(e, "pa_attention_key_weights");
+    tc = 2 * int64_t(num_kv_heads) * ((max_context_len - 1) / 128 + 1) >= sms;
+  }
+  if (tc) {
+    st = head_dim == 128 ? encode_pool_tile_map(&maps.k4, k_cache, *cache)
+                         : encode_pool_map(&maps.k2, k_cache, *cache);
+    if (st != PA_OK) return st;
+    if ((st = encode_q_map(&maps.q3, q, num_q_tokens, num_q_heads, head_dim,
+                           num_q_heads / num_kv_heads)) != PA_OK)
+      return st;
+  }
+  const cudaError_t e = pa::launch_key_weights(a, tc ? &maps : nullptr, stream);
   if (e != cudaSuccess) return cuda_fail(e, "pa_attention_key_weights launch");
   return PA_OK;
 }

@@ -413,7 +413,7 @@ cudaError_t run_key_weights(const KeyWeightsArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t stream) {
+cudaError_t launch_key_weights(const KeyWeightsArgs& a, const PoolMaps* maps, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (a.scores) {
     const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
@@ -426,6 +426,7 @@ cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t stream) {
   if (!a.k_pass) return cudaSuccess;
   e = launch_dependent(kw_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
   if (e != cudaSuccess) return e;
+  if (maps) return launch_key_weights_tc(a, *maps, stream);
   if (a.cache_dtype == PA_FP8_E4M3) return run_key_weights<Pool::kE4m3, 128>(a, stream);
   if (a.cache_dtype == PA_MXFP4)
     return a.head_dim == 128 ? run_key_weights<Pool::kMx, 128>(a, stream)

@@ -212,8 +212,14 @@ struct KeyWeightsArgs {
   int32_t num_q_heads, num_kv_heads, head_dim, cache_dtype;
   int32_t num_weight_rows, max_keys;
   float score_log2, decay;
+  uint64_t wait_ns;         // limit of every bounded wait
+  int32_t skip_copy;        // test hook (pa_test_skip_one_copy)
 };
-cudaError_t launch_key_weights(const KeyWeightsArgs& a, cudaStream_t stream);
+struct PoolMaps;
+// `maps`: of q and K for the tensor-core kernel (bf16 pools with enough items), or NULL.
+cudaError_t launch_key_weights(const KeyWeightsArgs& a, const PoolMaps* maps, cudaStream_t stream);
+cudaError_t launch_key_weights_tc(const KeyWeightsArgs& a, const PoolMaps& maps,
+                                  cudaStream_t stream);
 
 struct DecodeParams;
 // MXFP4 pools (decode_mx.cu): row tiles of 8 rows of an item, and the attention kernel.

@@ -391,6 +391,55 @@ def test_key_weights_of_a_step_whose_scores_are_not_kept():
     check_weights(c, np.zeros(W.shape, np.float32), W.cpu().numpy(), [0, 1, 2], 1.0)
 
 
+@pytest.mark.parametrize("d,hq,hkv", [(128, 16, 16), (64, 16, 16), (128, 64, 16), (128, 40, 20), (64, 128, 16)])
+def test_key_weights_of_chunks_on_the_tensor_cores(d, hq, hkv):
+    """Enough key chunks for a CTA each: long runs beside short ones, a chunk without a prefix, runs
+    that end inside a tile, keys that end inside a block, and a block outside the pool."""
+    import paged_kv_cache_286_gb300 as pa
+    qlens, ctx = [200, 1, 33, 70, 0, 129], [1300, 500, 33, 900, 44, 641]
+    c = Case(ctx, qlens, hq, hkv, d, "bf16", seed=d + hq)
+    t, ctx, qsl = c.dev()
+    before = np.random.default_rng(2).random((6, hkv, 1301)).astype(np.float32)
+    W = torch.from_numpy(before).cuda()
+    ws = c.workspace(pa, True)
+    ws[256:] = 0xFF
+    pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, ctx, qsl, W, ws, decay=0.5, **c.hints())
+    assert pa.check_error(ws) == 0
+    check_weights(c, before, W.cpu().numpy(), list(range(6)), 0.5)
+    W2 = torch.from_numpy(before).cuda()
+    pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, ctx, qsl, W2, ws, decay=0.5, **c.hints())
+    assert torch.equal(W, W2)
+    t[3, 20] = -7
+    W2 = torch.from_numpy(before).cuda()
+    pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, ctx, qsl, W2, ws, decay=0.5, **c.hints())
+    assert pa.check_error(ws, raise_on_error=False) == 0x1
+    keep = [0, 1, 2, 4, 5]
+    assert torch.equal(W[keep], W2[keep])
+    assert torch.equal(W2[3, :, 320:336].cpu(), torch.from_numpy(before[3, :, 320:336] * np.float32(0.5)))
+
+
+def test_key_weights_wait_that_expires_reports_a_timeout():
+    import paged_kv_cache_286_gb300 as pa
+    c = Case([1300, 500], [200, 1], 16, 16, 64, "bf16", seed=3)
+    t, ctx, qsl = c.dev()
+    L = pa.library()
+    ws = c.workspace(pa, True)
+    want = torch.zeros(2, 16, 1300, device="cuda")
+    pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, ctx, qsl, want, ws, **c.hints())
+    W = torch.zeros_like(want)
+    try:
+        L.pa_set_wait_limit_ns(20_000_000)
+        L.pa_test_skip_one_copy(1)
+        pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, ctx, qsl, W, ws, **c.hints())
+        assert pa.check_error(ws, raise_on_error=False) & 0x8
+    finally:
+        L.pa_test_skip_one_copy(0)
+        L.pa_set_wait_limit_ns(0)
+    W.zero_()
+    pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, ctx, qsl, W, ws, **c.hints())
+    assert pa.check_error(ws) == 0 and torch.equal(W, want)
+
+
 def test_key_weights_rows_left_out():
     import paged_kv_cache_286_gb300 as pa
     c = Case([40, 70, 33], [1, 2, 1], 4, 2, 64, "bf16", seed=2)
