@@ -5,11 +5,11 @@
 //
 //  * The scores of 128 keys and 128 rows are one accumulator of S^T = K Q^T: the keys are M, so that
 //    a key is a TMEM lane and its sum over rows stays in the two threads that read that lane (one
-//    per half of the columns) from the first row to the last.  No maximum, no exchange per tile, and
-//    no atomics: the two halves meet once per item, in a fixed order.
+//    per half of the columns, of even and of odd tiles) from the first row to the last.  No maximum,
+//    no exchange per tile, and no atomics: the four sums meet once per item, in a fixed order.
 //  * A CTA holds an item's keys (128 of one kv head, 32 KiB) while the rows pass: 128 / G tokens x
 //    G heads a tile, one 3-D TMA box per 64 columns, three tiles in flight; four accumulators let
-//    the MMAs run ahead of the epilogue.  Warp 0 copies, warp 1 issues the MMAs, warps 2-9 read the
+//    the MMAs run ahead of the epilogue.  Warp 0 copies, warp 1 issues the MMAs, warps 2-17 read the
 //    accumulators.  The next item's keys land while the last tiles of this one are summed.
 //  * A score costs the epilogue half a packed FMA, one 2^x and half a packed add: the 2^x, 16,384 a
 //    tile, is what bounds it (the MMAs of a tile take a quarter of that).
@@ -18,6 +18,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
@@ -26,8 +27,8 @@ namespace pa {
 
 namespace {
 
-constexpr int kTcThreads = 320;
-constexpr int kTcEpilogue = 8;           // warps 2 .. 9
+constexpr int kTcEpilogue = 16;          // warps 2 .. 17: two groups of eight, tile by tile in turn
+constexpr int kTcThreads = 32 * (2 + kTcEpilogue);
 constexpr int kTcQStages = 3, kTcKStages = 2, kTcBufs = 4;
 constexpr uint32_t kTcCols = 512;        // tensor memory: four accumulators of 128 columns
 
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ TcCtl ctl;
   __shared__ __align__(16) float s_lse[kTcEpilogue][64];  // negated, of each warp's columns
-  __shared__ float s_half[2][128];                        // sums of the two halves of the columns
+  __shared__ float s_part[4][128];  // sums by group and half of the columns
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kTcKStages; ++i) {
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < kTcBufs; ++i) {
       mbar_init(&ctl.d_full[i], 1);
-      mbar_init(&ctl.d_empty[i], kTcEpilogue);
+      mbar_init(&ctl.d_empty[i], kTcEpilogue / 2);
     }
     mbar_init(&ctl.sum_full, kTcEpilogue);
     mbar_init(&ctl.sum_free, kTcEpilogue);
@@ -205,7 +206,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_wait(&ctl.drain, 0, a.wait_ns);  // no MMA is in flight when the CTA ends
   } else {
     // ---------------------------------------------------------------- epilogue
-    const int e = warp - 2, half = e >> 2, quarter = warp & 3;  // TMEM lane quarter of the warp
+    const int e = warp - 2, group = e >> 3, half = (e >> 2) & 1;
+    const int quarter = warp & 3;                               // TMEM lane quarter of the warp
     const int k = quarter * 32 + lane;                          // key of the item = TMEM lane
     const uint32_t cols = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 64u;
     const f32x2 scale2 = f2_pack(a.score_log2, a.score_log2);
@@ -222,63 +224,75 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                    ? -a.lse[static_cast<int64_t>(I.t0 + tok) * a.num_q_heads + I.h * G + g]
                    : -CUDART_INF_F;
       };
-      float next0 = lse_of(0, tok_0, g_0), next1 = lse_of(0, tok_1, g_1);
+      const int first = static_cast<int>((qc ^ group) & 1u);  // the group's first tile of the item
+      float next0 = lse_of(first, tok_0, g_0), next1 = lse_of(first, tok_1, g_1);
       f32x2 sum[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
-      for (int t = 0; t < I.tiles; ++t, ++qc) {
-        const uint32_t b = qc % kTcBufs;
+      for (int t = first; t < I.tiles; t += 2) {
+        const uint32_t b = (qc + t) % kTcBufs;
         __syncwarp();
         s_lse[e][lane] = next0;
         s_lse[e][lane + 32] = next1;
         __syncwarp();
-        next0 = lse_of(t + 1, tok_0, g_0);
-        next1 = lse_of(t + 1, tok_1, g_1);
-        if (!(ok = wait(&ctl.d_full[b], (qc / kTcBufs) & 1u))) break;
+        next0 = lse_of(t + 2, tok_0, g_0);
+        next1 = lse_of(t + 2, tok_1, g_1);
+        if (!(ok = wait(&ctl.d_full[b], ((qc + t) / kTcBufs) & 1u))) break;
         tc_fence_after();
-        uint32_t acc[64];
-        tmem_ld32(cols + b * 128u, *reinterpret_cast<uint32_t(*)[32]>(&acc[0]));
-        tmem_ld32(cols + b * 128u + 32u, *reinterpret_cast<uint32_t(*)[32]>(&acc[32]));
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.d_empty[b]);
         // columns of rows that see the key: from `from` on, and rows of the run only
         const int tok0 = I.first_tok + t * tpt;
         const int from = (key - (I.L - I.n) - tok0) * G - half * 64;
         const int upto = min(64, (I.n - tok0) * G - half * 64);
         const bool all = __all_sync(0xffffffffu, from <= 0) && upto == 64;
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(&s_lse[e][c]);
-          f32x2 x0 = f2_fma(f2_pack(__uint_as_float(acc[c]), __uint_as_float(acc[c + 1])), scale2,
-                            f2_pack(l.x, l.y));
-          f32x2 x1 = f2_fma(f2_pack(__uint_as_float(acc[c + 2]), __uint_as_float(acc[c + 3])),
-                            scale2, f2_pack(l.z, l.w));
-          float w[4];
-          f2_unpack(x0, w[0], w[1]);
-          f2_unpack(x1, w[2], w[3]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = fast_exp2(w[i]);
-          if (!all) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = c + i >= from && c + i < upto ? w[i] : 0.f;
+        for (int c0 = 0; c0 < 64; c0 += 32) {
+          uint32_t acc[32];
+          tmem_ld32(cols + b * 128u + c0, acc);
+          tmem_wait_ld();
+          if (c0 == 32) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.d_empty[b]);
           }
-          sum[(c >> 2) & 1] = f2_add(sum[(c >> 2) & 1], f2_pack(w[0], w[1]));
-          sum[2 + ((c >> 2) & 1)] = f2_add(sum[2 + ((c >> 2) & 1)], f2_pack(w[2], w[3]));
+          auto add = [&](auto all_tag) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(&s_lse[e][c0 + c]);
+              const f32x2 x0 = f2_fma(
+                  f2_pack(__uint_as_float(acc[c]), __uint_as_float(acc[c + 1])), scale2,
+                  f2_pack(l.x, l.y));
+              const f32x2 x1 = f2_fma(
+                  f2_pack(__uint_as_float(acc[c + 2]), __uint_as_float(acc[c + 3])), scale2,
+                  f2_pack(l.z, l.w));
+              float w[4];
+              f2_unpack(x0, w[0], w[1]);
+              f2_unpack(x1, w[2], w[3]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                w[i] = fast_exp2(w[i]);
+                if (!decltype(all_tag)::value)
+                  w[i] = c0 + c + i >= from && c0 + c + i < upto ? w[i] : 0.f;
+              }
+              sum[(c >> 2) & 1] = f2_add(sum[(c >> 2) & 1], f2_pack(w[0], w[1]));
+              sum[2 + ((c >> 2) & 1)] = f2_add(sum[2 + ((c >> 2) & 1)], f2_pack(w[2], w[3]));
+            }
+          };
+          if (all) add(std::true_type());
+          else add(std::false_type());
         }
       }
+      qc += I.tiles;
       if (!ok) break;
       float lo, hi;
       f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), lo, hi);
       // the sums of the item before are read
       if (kc > 0 && !(ok = wait(&ctl.sum_free, (kc - 1) & 1u))) break;
-      s_half[half][k] = lo + hi;
+      s_part[2 * group + half][k] = lo + hi;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.sum_full);
       if (!(ok = wait(&ctl.sum_full, kc & 1u))) break;
-      if (half == 0 && key < I.L) {
-        float x = s_half[0][k] + s_half[1][k];
+      if (e < 4 && key < I.L) {
+        float x = (s_part[0][k] + s_part[1][k]) + (s_part[2][k] + s_part[3][k]);
         const int phys = __ldg(a.block_tables + static_cast<int64_t>(I.s) * a.max_blocks_per_seq +
                                key / kBlockSize);
         // keys of bad blocks, which the attention leaves out, receive nothing
