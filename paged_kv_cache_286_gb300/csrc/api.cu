@@ -677,7 +677,7 @@ pa_status pa_attention_key_weights(
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_fail(e, "pa_attention_key_weights");
-    tc = 2 * int64_t(num_kv_heads) * ((max_context_len - 1) / 128 + 1) >= sms;
+    tc = 2 * int64_t(num_kv_heads) * ((max_context_len - 1) / pa::kKeyWeightsTcKeys + 1) >= sms;
   }
   if (tc) {
     st = head_dim == 128 ? encode_pool_tile_map(&maps.k4, k_cache, *cache)

@@ -58,7 +58,7 @@ __device__ __forceinline__ bool kw_accumulates(const KeyWeightsArgs& a, int s,
 __device__ __forceinline__ int kw_chunks(const KeyWeightsArgs& a, int s, uint32_t* err_bits) {
   if (!kw_accumulates(a, s, err_bits)) return 0;
   if ((a.qsl[s + 1] - a.qsl[s]) * (a.num_q_heads / a.num_kv_heads) <= a.score_rows) return 0;
-  return (a.context_lens[s] + kKwKeys - 1) / kKwKeys;
+  return (a.context_lens[s] + a.chunk_keys - 1) / a.chunk_keys;
 }
 
 // Runs whose scores the attention kept: one CTA per (sequence, kv head) and equal share of its
@@ -413,7 +413,8 @@ cudaError_t run_key_weights(const KeyWeightsArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_key_weights(const KeyWeightsArgs& a, const PoolMaps* maps, cudaStream_t stream) {
+cudaError_t launch_key_weights(KeyWeightsArgs a, const PoolMaps* maps, cudaStream_t stream) {
+  a.chunk_keys = maps ? kKeyWeightsTcKeys : kKwKeys;
   cudaError_t e = cudaSuccess;
   if (a.scores) {
     const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;

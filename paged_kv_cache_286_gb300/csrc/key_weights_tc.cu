@@ -5,14 +5,13 @@
 //
 //  * The scores of 128 keys and 128 rows are one accumulator of S^T = K Q^T: the keys are M, so that
 //    a key is a TMEM lane and its sum over rows stays in the two threads that read that lane (one
-//    per half of the columns, of even and of odd tiles) from the first row to the last.  No maximum,
-//    no exchange per tile, and no atomics: the four sums meet once per item, in a fixed order.
-//  * A CTA holds an item's keys (128 of one kv head, 32 KiB) while the rows pass: 128 / G tokens x
-//    G heads a tile, one 3-D TMA box per 64 columns, three tiles in flight; four accumulators let
-//    the MMAs run ahead of the epilogue.  Warp 0 copies, warp 1 issues the MMAs, warps 2-17 read the
-//    accumulators.  The next item's keys land while the last tiles of this one are summed.
-//  * A score costs the epilogue half a packed FMA, one 2^x and half a packed add: the 2^x, 16,384 a
-//    tile, is what bounds it (the MMAs of a tile take a quarter of that).
+//    per half of the columns) from the first row to the last.  No maximum, no exchange per tile, and
+//    no atomics: the two halves meet once per item, in a fixed order.
+//  * A CTA holds an item's keys (256 of one kv head, 64 KiB, two accumulators) while the rows pass:
+//    128 / G tokens x G heads a tile, one 3-D TMA box per 64 columns, four tiles in flight, two pairs
+//    of accumulators.  Warp 0 copies, warp 1 issues the MMAs, warps 2-17 read the accumulators.
+//  * A score costs the epilogue an FMA, a 2^x and an add; the 2^x bound it from below (32 a cycle
+//    and SM: 0.5 us a tile of 256 x 128), the MMAs take about as long.
 //  * Every wait is bounded; when one runs out the CTA records PA_DEVERR_TIMEOUT, stops, lets its
 //    copies and MMAs finish (bounded again) and frees its tensor memory.
 #include <math_constants.h>
@@ -27,16 +26,18 @@ namespace pa {
 
 namespace {
 
-constexpr int kTcEpilogue = 16;          // warps 2 .. 17: two groups of eight, tile by tile in turn
+constexpr int kTcKeys = kKeyWeightsTcKeys;  // keys of an item: two accumulators' rows
+static_assert(kTcKeys == 256, "two accumulators of 128 lanes");
+constexpr int kTcEpilogue = 16;             // warps 2 .. 17: eight for each 128 keys
 constexpr int kTcThreads = 32 * (2 + kTcEpilogue);
-constexpr int kTcQStages = 3, kTcKStages = 2, kTcBufs = 4;
-constexpr uint32_t kTcCols = 512;        // tensor memory: four accumulators of 128 columns
+constexpr int kTcQStages = 4, kTcKStages = 1, kTcBufs = 2;
+constexpr uint32_t kTcCols = 512;           // tensor memory: two pairs of accumulators of 128 columns
 
 template <int D>
 struct TcLayout {
   static constexpr int kTile = 128 * D * 2;  // 128 keys or rows
   static constexpr int kK = 0;
-  static constexpr int kQ = kTcKStages * kTile;
+  static constexpr int kQ = kTcKStages * 2 * kTile;
   static constexpr int kSmem = 1024 + kQ + kTcQStages * kTile;
 };
 
@@ -66,7 +67,7 @@ __device__ __forceinline__ TcItem tc_item(const KeyWeightsArgs& a, int64_t item,
   it.t0 = a.qsl[lo];
   it.n = a.qsl[lo + 1] - it.t0;
   it.L = a.context_lens[lo];
-  it.base = (chunk_id - a.chunk_start[lo]) * 128;
+  it.base = (chunk_id - a.chunk_start[lo]) * kTcKeys;
   it.first_tok = max(0, it.base - (it.L - it.n));  // the first that sees some key of the item
   it.tiles = (it.n - it.first_tok + tpt - 1) / tpt;
   return it;
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ TcCtl ctl;
   __shared__ __align__(16) float s_lse[kTcEpilogue][64];  // negated, of each warp's columns
-  __shared__ float s_part[4][128];  // sums by group and half of the columns
+  __shared__ float s_part[2][kTcKeys];  // sums by half of the columns
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kTcKStages; ++i) {
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < kTcBufs; ++i) {
       mbar_init(&ctl.d_full[i], 1);
-      mbar_init(&ctl.d_empty[i], kTcEpilogue / 2);
+      mbar_init(&ctl.d_empty[i], kTcEpilogue);
     }
     mbar_init(&ctl.sum_full, kTcEpilogue);
     mbar_init(&ctl.sum_free, kTcEpilogue);
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t ks = kc % kTcKStages;
       const int jb = I.base / kBlockSize + lane;  // this lane's block of the keys
       int phys = -1;
-      if (lane < 8 && jb * kBlockSize < I.L) {
+      if (lane < kTcKeys / kBlockSize && jb * kBlockSize < I.L) {
         phys = __ldg(a.block_tables + static_cast<int64_t>(I.s) * a.max_blocks_per_seq + jb);
         if (phys >= a.num_blocks) phys = -1;  // (flagged by the attention)
       }
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       __syncwarp();
       // test hook: the first item's first copy is left out while its bytes are expected
       if (phys >= 0 && !(a.skip_copy && item == 0 && lane == 0)) {
-        uint8_t* dst = smem + L::kK + ks * L::kTile + lane * (kBlockSize * D * 2);
+        uint8_t* dst = smem + L::kK + ks * 2 * L::kTile + lane * (kBlockSize * D * 2);
         const int group = (phys * a.num_kv_heads + I.h) * 2;  // its first group of 8 pool rows
         if constexpr (D == 128) tma_load_4d(dst, &kmap, 0, 0, 0, group, &ctl.k_full[ks]);
         else tma_load_2d(dst, &kmap, 0, group * 8, &ctl.k_full[ks]);
@@ -183,17 +184,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!(ok = wait(&ctl.q_full[qs], (qc / kTcQStages) & 1u))) break;
         tc_fence_after();
         if (lane == 0) {
-          const uint32_t k_addr = smem_u32(smem + L::kK + ks * L::kTile);
+          const uint32_t k_addr = smem_u32(smem + L::kK + ks * 2 * L::kTile);
           const uint32_t q_addr = smem_u32(smem + L::kQ + qs * L::kTile);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            // 64-column halves of a K block 1 KiB apart (8-key groups 2 KiB apart; one half for
-            // head_dim 64: 1 KiB), of the q tile 16 KiB apart (8-row groups 1 KiB apart)
-            tc_mma_bf16(tmem + b * 128u,
-                        smem_desc_sw128(k_addr + (k >> 2) * 1024 + (k & 3) * 32, 16,
-                                        D == 128 ? 2048 : 1024),
-                        smem_desc_sw128(q_addr + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024), idesc,
-                        k > 0);
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              // 64-column halves of a K block 1 KiB apart (8-key groups 2 KiB apart; one half for
+              // head_dim 64: 1 KiB), of the q tile 16 KiB apart (8-row groups 1 KiB apart)
+              tc_mma_bf16(tmem + b * 256u + m * 128u,
+                          smem_desc_sw128(k_addr + m * L::kTile + (k >> 2) * 1024 + (k & 3) * 32, 16,
+                                          D == 128 ? 2048 : 1024),
+                          smem_desc_sw128(q_addr + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024), idesc,
+                          k > 0);
           tc_commit(&ctl.d_full[b]);
           tc_commit(&ctl.q_empty[qs]);
           if (t == I.tiles - 1) tc_commit(&ctl.k_empty[ks]);
@@ -206,11 +209,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_wait(&ctl.drain, 0, a.wait_ns);  // no MMA is in flight when the CTA ends
   } else {
     // ---------------------------------------------------------------- epilogue
-    const int e = warp - 2, group = e >> 3, half = (e >> 2) & 1;
-    const int quarter = warp & 3;                               // TMEM lane quarter of the warp
-    const int k = quarter * 32 + lane;                          // key of the item = TMEM lane
-    const uint32_t cols = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 64u;
-    const f32x2 scale2 = f2_pack(a.score_log2, a.score_log2);
+    const int e = warp - 2, m = e >> 3, half = (e >> 2) & 1;
+    const int quarter = warp & 3;                 // TMEM lane quarter of the warp
+    const int k = m * 128 + quarter * 32 + lane;  // key of the item: TMEM lane of accumulator m
+    const uint32_t cols = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + m * 128u + half * 64u;
+    const float scale = a.score_log2;
     // token and head, within a tile, of this lane's two columns of the warp's 64
     const int r0 = half * 64 + lane, r1 = r0 + 32;
     const int tok_0 = r0 / G, g_0 = r0 - tok_0 * G, tok_1 = r1 / G, g_1 = r1 - tok_1 * G;
@@ -224,20 +227,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                    ? -a.lse[static_cast<int64_t>(I.t0 + tok) * a.num_q_heads + I.h * G + g]
                    : -CUDART_INF_F;
       };
-      const int first = static_cast<int>((qc ^ group) & 1u);  // the group's first tile of the item
-      float next0 = lse_of(first, tok_0, g_0), next1 = lse_of(first, tok_1, g_1);
-      f32x2 sum[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum[i] = f2_pack(0.f, 0.f);
-      for (int t = first; t < I.tiles; t += 2) {
-        const uint32_t b = (qc + t) % kTcBufs;
+      float next0 = lse_of(0, tok_0, g_0), next1 = lse_of(0, tok_1, g_1);
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < I.tiles; ++t, ++qc) {
+        const uint32_t b = qc % kTcBufs;
         __syncwarp();
         s_lse[e][lane] = next0;
         s_lse[e][lane + 32] = next1;
         __syncwarp();
-        next0 = lse_of(t + 2, tok_0, g_0);
-        next1 = lse_of(t + 2, tok_1, g_1);
-        if (!(ok = wait(&ctl.d_full[b], ((qc + t) / kTcBufs) & 1u))) break;
+        next0 = lse_of(t + 1, tok_0, g_0);
+        next1 = lse_of(t + 1, tok_1, g_1);
+        if (!(ok = wait(&ctl.d_full[b], (qc / kTcBufs) & 1u))) break;
         tc_fence_after();
         // columns of rows that see the key: from `from` on, and rows of the run only
         const int tok0 = I.first_tok + t * tpt;
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int c0 = 0; c0 < 64; c0 += 32) {
           uint32_t acc[32];
-          tmem_ld32(cols + b * 128u + c0, acc);
+          tmem_ld32(cols + b * 256u + c0, acc);
           tmem_wait_ld();
           if (c0 == 32) {
             tc_fence_before();
@@ -258,41 +258,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int c = 0; c < 32; c += 4) {
               const float4 l = *reinterpret_cast<const float4*>(&s_lse[e][c0 + c]);
-              const f32x2 x0 = f2_fma(
-                  f2_pack(__uint_as_float(acc[c]), __uint_as_float(acc[c + 1])), scale2,
-                  f2_pack(l.x, l.y));
-              const f32x2 x1 = f2_fma(
-                  f2_pack(__uint_as_float(acc[c + 2]), __uint_as_float(acc[c + 3])), scale2,
-                  f2_pack(l.z, l.w));
-              float w[4];
-              f2_unpack(x0, w[0], w[1]);
-              f2_unpack(x1, w[2], w[3]);
+              const float v[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                w[i] = fast_exp2(w[i]);
-                if (!decltype(all_tag)::value)
-                  w[i] = c0 + c + i >= from && c0 + c + i < upto ? w[i] : 0.f;
+                const float w = fast_exp2(fmaf(__uint_as_float(acc[c + i]), scale, v[i]));
+                if (decltype(all_tag)::value || (c0 + c + i >= from && c0 + c + i < upto)) sum[i] += w;
               }
-              sum[(c >> 2) & 1] = f2_add(sum[(c >> 2) & 1], f2_pack(w[0], w[1]));
-              sum[2 + ((c >> 2) & 1)] = f2_add(sum[2 + ((c >> 2) & 1)], f2_pack(w[2], w[3]));
             }
           };
           if (all) add(std::true_type());
           else add(std::false_type());
         }
       }
-      qc += I.tiles;
       if (!ok) break;
-      float lo, hi;
-      f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), lo, hi);
       // the sums of the item before are read
       if (kc > 0 && !(ok = wait(&ctl.sum_free, (kc - 1) & 1u))) break;
-      s_part[2 * group + half][k] = lo + hi;
+      s_part[half][k] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.sum_full);
       if (!(ok = wait(&ctl.sum_full, kc & 1u))) break;
-      if (e < 4 && key < I.L) {
-        float x = (s_part[0][k] + s_part[1][k]) + (s_part[2][k] + s_part[3][k]);
+      if (half == 0 && key < I.L) {
+        float x = s_part[0][k] + s_part[1][k];
         const int phys = __ldg(a.block_tables + static_cast<int64_t>(I.s) * a.max_blocks_per_seq +
                                key / kBlockSize);
         // keys of bad blocks, which the attention leaves out, receive nothing
@@ -318,7 +304,7 @@ cudaError_t run_tc(const KeyWeightsArgs& a, const PoolMaps& maps, cudaStream_t s
   cudaError_t e = launch_info(kern, kTcThreads, TcLayout<D>::kSmem, &li);
   if (e != cudaSuccess) return e;
   const int64_t upper = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads *
-                        ((a.max_context_len + int64_t(127)) / 128);
+                        ((a.max_context_len + int64_t(kTcKeys) - 1) / kTcKeys);
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(upper, li.sms));
   return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kTcThreads),
                           TcLayout<D>::kSmem, stream, maps.q3, D == 128 ? maps.k4 : maps.k2, a);

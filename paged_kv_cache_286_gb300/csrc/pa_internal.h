@@ -203,6 +203,7 @@ struct KeyWeightsArgs {
   const float* lse;         // [T][Hq], log2 domain
   const float* scores;      // of the runs of up to score_rows rows (DecodeParams), or NULL
   int32_t score_rows, score_stride;
+  int32_t chunk_keys;       // keys of an item of that kernel (set by launch_key_weights)
   int32_t k_pass;           // some run may have more rows than that: the kernel that reads K runs
   const int32_t* weight_rows;
   float* key_weights;       // [num_weight_rows][Hkv][max_keys]
@@ -217,7 +218,8 @@ struct KeyWeightsArgs {
 };
 struct PoolMaps;
 // `maps`: of q and K for the tensor-core kernel (bf16 pools with enough items), or NULL.
-cudaError_t launch_key_weights(const KeyWeightsArgs& a, const PoolMaps* maps, cudaStream_t stream);
+constexpr int kKeyWeightsTcKeys = 256;  // keys of an item of the tensor-core kernel
+cudaError_t launch_key_weights(KeyWeightsArgs a, const PoolMaps* maps, cudaStream_t stream);
 cudaError_t launch_key_weights_tc(const KeyWeightsArgs& a, const PoolMaps& maps,
                                   cudaStream_t stream);
 
