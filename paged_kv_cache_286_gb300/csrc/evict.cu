@@ -11,8 +11,9 @@
 //    kept positions and weights.
 //  * move_kernel: one CTA per (sequence, kv head, K or V, column slice).  A kept key never moves
 //    up, so rows can move in place if a batch of them is read before it is written and batches go
-//    in order: every source of a later batch lies above all that is written so far.  The rows of
-//    the next batch are looked up while a batch's loads are in flight.
+//    in order: every source of a later batch lies above all that is written so far.  Positions,
+//    table entries and rows are loads that wait on one another; they run two, one and no batches
+//    ahead.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -217,7 +218,7 @@ constexpr int kMovePer = 4;  // 16-byte pieces of a thread in a batch
 // vec: 16-byte pieces of a row's slice.  MXFP4 rows (kNB > 0) also have kNB scale bytes, which the
 // threads with the row's first piece move.
 template <int kNB>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, int row_bytes,
+__global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const EvictArgs a, int row_bytes,
                                                             int slices, int vec_log2) {
   grid_dependency_wait();
   int id = blockIdx.x;
@@ -247,56 +248,68 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
     return pool + static_cast<int64_t>(row >> 4) * (kBlockSize * (row_bytes + kNB)) +
            kBlockSize * row_bytes + (row & 15) * kNB;
   };
-  int32_t from[2][kMovePer], to[2][kMovePer];  // pool rows (fewer than 2^31) of a batch; -1: none
+  // Of a batch, in three steps that each wait on the one before, so each runs an iteration ahead
+  // of the next: the kept positions, the table entries, the rows themselves.
+  int32_t j_of[kMovePer], from_b[kMovePer], to_b[kMovePer];
+  int32_t from[kMovePer], to[kMovePer];  // pool rows (fewer than 2^31); -1: none
   uint4 x[kMovePer];
   uint32_t sc[kMovePer];
-  auto find = [&](int buf, int first) {
+  auto positions = [&](int first) {
 #pragma unroll
     for (int i = 0; i < kMovePer; ++i) {
       const int at = first + my_row + i * row_step;
-      from[buf][i] = to[buf][i] = -1;
-      if (at < e.k) {
-        const int j = kept[at];
-        const int from_b = __ldg(src_t + j / kBlockSize), to_b = __ldg(dst_t + at / kBlockSize);
-        if (from_b < 0 || from_b >= a.num_blocks || to_b < 0 || to_b >= a.num_blocks) {
-          set_error(a.err, PA_DEVERR_BLOCK_ID);
-        } else if (from_b != to_b || j % kBlockSize != at % kBlockSize) {
-          from[buf][i] = (from_b * a.num_kv_heads + h) * kBlockSize + j % kBlockSize;
-          to[buf][i] = (to_b * a.num_kv_heads + h) * kBlockSize + at % kBlockSize;
-        }
+      j_of[i] = at < e.k ? kept[at] : -1;
+    }
+  };
+  int32_t j_in[kMovePer];  // positions of the entries in from_b / to_b
+  auto entries = [&](int first) {
+#pragma unroll
+    for (int i = 0; i < kMovePer; ++i) {
+      const int at = first + my_row + i * row_step;
+      j_in[i] = j_of[i];
+      if (j_in[i] >= 0) {
+        from_b[i] = __ldg(src_t + j_in[i] / kBlockSize);
+        to_b[i] = __ldg(dst_t + at / kBlockSize);
       }
     }
   };
-  auto load = [&](int buf) {
+  auto rows_of = [&](int first) {
 #pragma unroll
     for (int i = 0; i < kMovePer; ++i) {
-      if (from[buf][i] < 0) continue;
-      x[i] = *reinterpret_cast<const uint4*>(pool + offset(from[buf][i]) + col);
-      if (kNB == 4 && col == 0) sc[i] = *reinterpret_cast<const uint32_t*>(scales(from[buf][i]));
-      if (kNB == 2 && col == 0) sc[i] = *reinterpret_cast<const uint16_t*>(scales(from[buf][i]));
+      const int at = first + my_row + i * row_step;
+      from[i] = to[i] = -1;
+      if (j_in[i] < 0) continue;
+      if (from_b[i] < 0 || from_b[i] >= a.num_blocks || to_b[i] < 0 || to_b[i] >= a.num_blocks) {
+        set_error(a.err, PA_DEVERR_BLOCK_ID);
+      } else if (from_b[i] != to_b[i] || j_in[i] % kBlockSize != at % kBlockSize) {
+        from[i] = (from_b[i] * a.num_kv_heads + h) * kBlockSize + j_in[i] % kBlockSize;
+        to[i] = (to_b[i] * a.num_kv_heads + h) * kBlockSize + at % kBlockSize;
+      }
     }
   };
-  auto store = [&](int buf) {
+  positions(0);
+  entries(0);
+  positions(rows);
+  for (int first = 0; first < e.k; first += rows) {
+    rows_of(first);
 #pragma unroll
     for (int i = 0; i < kMovePer; ++i) {
-      if (to[buf][i] < 0) continue;
-      *reinterpret_cast<uint4*>(pool + offset(to[buf][i]) + col) = x[i];
-      if (kNB == 4 && col == 0) *reinterpret_cast<uint32_t*>(scales(to[buf][i])) = sc[i];
+      if (from[i] < 0) continue;
+      x[i] = *reinterpret_cast<const uint4*>(pool + offset(from[i]) + col);
+      if (kNB == 4 && col == 0) sc[i] = *reinterpret_cast<const uint32_t*>(scales(from[i]));
+      if (kNB == 2 && col == 0) sc[i] = *reinterpret_cast<const uint16_t*>(scales(from[i]));
+    }
+    entries(first + rows);
+    positions(first + 2 * rows);
+    __syncthreads();  // everyone has loaded the batch
+#pragma unroll
+    for (int i = 0; i < kMovePer; ++i) {
+      if (to[i] < 0) continue;
+      *reinterpret_cast<uint4*>(pool + offset(to[i]) + col) = x[i];
+      if (kNB == 4 && col == 0) *reinterpret_cast<uint32_t*>(scales(to[i])) = sc[i];
       if (kNB == 2 && col == 0)
-        *reinterpret_cast<uint16_t*>(scales(to[buf][i])) = static_cast<uint16_t>(sc[i]);
+        *reinterpret_cast<uint16_t*>(scales(to[i])) = static_cast<uint16_t>(sc[i]);
     }
-  };
-  find(0, 0);
-  for (int first = 0; first < e.k; first += 2 * rows) {
-    // a batch is loaded, the next one's rows are found, and once everyone has loaded it is stored
-    load(0);
-    find(1, first + rows);
-    __syncthreads();
-    store(0);
-    load(1);
-    find(0, first + 2 * rows);
-    __syncthreads();
-    store(1);
   }
 }
 
