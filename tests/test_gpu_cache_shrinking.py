@@ -552,23 +552,35 @@ def test_evict(weights, kind, d, hkv, in_place):
         assert np.array_equal(tile_rows(c.k, kind, d), k_w) and np.array_equal(tile_rows(c.v, kind, d), v_w)
 
 
-def test_evict_long_rows_and_default_rows():
+@pytest.mark.parametrize("weights", ["random", "ties", "odd", "equal"])
+@pytest.mark.parametrize("ctx,keep,hkv", [
+    ([70000, 65537], [30011, 65536], 1),          # more than a CTA's shared memory holds
+    ([9000, 4097, 1, 40, 8191, 16], [1, 4096, 1, 0, 8190, 16], 2),
+    ([5000, 300, 4999], [2500, 299, 4999], 1),
+    ([450000, 17], [200000, 3], 1),
+])
+def test_evict_long_rows_and_default_rows(ctx, keep, hkv, weights):
     import paged_kv_cache_286_gb300 as pa
-    c = Case([70000, 65537], [1, 1], 1, 1, 64, "bf16", seed=12)
+    c = Case(ctx, [1] * len(ctx), hkv, hkv, 64, "bf16", seed=12)
     rng = np.random.default_rng(5)
-    W = rng.random((2, 1, 70001)).astype(np.float32) ** 8
-    keep = np.array([30011, 65536], np.int32)
-    args = evict_reference(c, W, c.ctx, keep, 555, 65536, c.tables, [0, 1], [0, 1])
-    Wt = torch.from_numpy(W).cuda()
-    ws = pa.new_workspace(pa.evict_workspace_size(2, 1, 70000, 65536))
-    t, ctx, _ = c.dev()
-    kept, lens = pa.evict_keys(c.k, c.v, t, ctx, torch.from_numpy(keep).cuda(), Wt, ws, max_context_len=70000,
-                               max_keep_len=65536, recent=555)
-    assert pa.check_error(ws) == 0
-    for got, want in zip((kept, lens, Wt), (args[0], args[1], args[4])):
-        assert np.array_equal(got.cpu().numpy(), want)
-    assert np.array_equal(tile_rows(c.k, "bf16", 64), args[2])
-    assert np.array_equal(tile_rows(c.v, "bf16", 64), args[3])
+    top = max(ctx)
+    W0 = WEIGHTS[weights](rng, (len(ctx), hkv, top + 1)).astype(np.float32)
+    if weights == "random":
+        W0 = W0 ** 8
+    keep = np.array(keep, np.int32)
+    rows = list(range(len(ctx)))
+    ws = pa.new_workspace(pa.evict_workspace_size(len(ctx), hkv, top, int(keep.max())))
+    t, lens, _ = c.dev()
+    for recent in (0, 555):
+        args = evict_reference(c, W0, c.ctx, keep, recent, int(keep.max()), c.tables, rows, rows)
+        k, v, Wt = c.k.clone(), c.v.clone(), torch.from_numpy(W0).cuda()
+        kept, new = pa.evict_keys(k, v, t, lens, torch.from_numpy(keep).cuda(), Wt, ws, max_context_len=top,
+                                  max_keep_len=int(keep.max()), recent=recent)
+        assert pa.check_error(ws) == 0
+        assert np.array_equal(kept.cpu().numpy(), args[0]) and np.array_equal(new.cpu().numpy(), args[1])
+        assert np.array_equal(Wt.cpu().numpy(), args[4], equal_nan=True)
+        assert np.array_equal(tile_rows(k, "bf16", 64), args[2])
+        assert np.array_equal(tile_rows(v, "bf16", 64), args[3])
 
 
 def test_evict_leaves_bad_sequences_as_they_are():
