@@ -1052,6 +1052,10 @@ cudaError_t launch_attention(const AttnArgs& a, const WsLayout& ws, const PoolMa
   p.num_blocks = a.cache.num_blocks;
   p.max_context_len = a.max_context_len;
   p.max_query_len = a.max_query_len;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p.sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
   // An E4M3 block is half the bytes of a bf16 one: give E4M3 items twice the blocks (the
   // workspace, sized for the bf16 choice, then holds fewer partitions than it has room for;
   // pmax stays the row stride of the partial arrays).  Fewer, longer partitions also make the
@@ -1059,12 +1063,16 @@ cudaError_t launch_attention(const AttnArgs& a, const WsLayout& ws, const PoolMa
   // A 4-bit block is a quarter of the bytes, and its items take up to four times the blocks.
   const bool fp8_cache = a.cache.cache_dtype == PA_FP8_E4M3;
   const bool mx = a.cache.cache_dtype == PA_MXFP4;
-  const int hpi = decode_heads_per_item(a.cache, a.num_q_heads, a.num_kv_heads,
-                                        a.max_query_len);
-  p.heads_per_item = hpi;
   p.pblk = ((fp8_cache || mx) && ws.pblk <= 32) ? ws.pblk * 2 : ws.pblk;
-  // a warp holds the table entries of its blocks of a partition one per lane
-  if (p.pblk > kDecodeWarps * 32) return cudaErrorInvalidValue;
+  int pblk2 = p.pblk;
+  const int hpi = mx ? mx_heads_per_item(a, p, ws.pblk, &pblk2)
+                     : decode_heads_per_item(a.cache, a.num_q_heads, a.num_kv_heads,
+                                             a.max_query_len);
+  p.heads_per_item = hpi;
+  if (mx && hpi == 2) p.pblk = pblk2;
+  // a warp holds the table entries of its blocks of a partition one per lane (of two 4-bit heads:
+  // two)
+  if (p.pblk > kDecodeWarps * 32 * (mx ? hpi : 1)) return cudaErrorInvalidValue;
   p.pmax = ws.pmax;
   const bool prefill = use_prefill && prefill_path_enabled(a.cache, a.num_q_heads,
                                                           a.num_kv_heads);
@@ -1092,10 +1100,6 @@ cudaError_t launch_attention(const AttnArgs& a, const WsLayout& ws, const PoolMa
   p.score_rows = a.score_rows;
   p.score_stride = a.score_stride;
 
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p.sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   p.kv_tile_bytes = mx ? 2 * a.head_dim * 17 / 2 : 2 * kBlockSize * a.head_dim * (fp8 ? 1 : 2);
   p.span = a.span;
 

@@ -46,7 +46,7 @@ constexpr int kDecodeMaxGroup = 16;      // q heads per kv head: up to 16 rows o
 constexpr int kDecodeMaxQuery = 16;       // sequences with n_s above this use the prefill path,
 constexpr int kDecodeMaxRows = 16;        // and so do those with more n_s x G rows than this
 
-constexpr int kMxMaxRows = 32;            // rows of the largest tile of the MXFP4 split-KV kernel
+constexpr int kMxMaxRows = 32;            // longer MXFP4 runs are staged for the prefill tiles
 
 // Whether a query run of n tokens with G heads per kv head is served by the prefill-tile
 // kernel (when that kernel is built for the pool): more rows than one 16-row decode tile holds

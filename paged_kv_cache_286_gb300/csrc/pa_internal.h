@@ -226,6 +226,7 @@ cudaError_t launch_key_weights_tc(const KeyWeightsArgs& a, const PoolMaps& maps,
 struct DecodeParams;
 // MXFP4 pools (decode_mx.cu): row tiles of 8 rows of an item, and the attention kernel.
 int mx_row_tiles(int32_t max_query_len, int32_t group);
+int mx_heads_per_item(const AttnArgs& a, const DecodeParams& p, int min_pblk, int* pblk);
 // Sequences with more rows than its tiles: bf16 copies of their keys and values.
 cudaError_t launch_mx_stage_plan(const AttnArgs& a, const DecodeParams& p);
 cudaError_t launch_mx_stage(const AttnArgs& a, const DecodeParams& p);

@@ -36,11 +36,12 @@ def bits_f64(t):
 class Case:
     """Pools of one kind with random contents (stale slots hold NaN patterns) and their values."""
 
-    def __init__(self, ctx, qlens, hq, hkv, d, kind, seed=0, spare=3, spread=0, cols=1):
+    def __init__(self, ctx, qlens, hq, hkv, d, kind, seed=0, spare=3, spread=0, cols=1, bound=0):
         rng = np.random.default_rng(seed)
         g = torch.Generator().manual_seed(seed)
         self.ctx, self.qlens = np.array(ctx, np.int32), np.array(qlens, np.int32)
         self.hq, self.hkv, self.d, self.kind = hq, hkv, d, kind
+        self.bound = max(bound, int(self.ctx.max()))                # max_context_len of the calls
         S = len(ctx)
         nblk = -(-self.ctx // BS)
         nb = int(nblk.sum()) + spare
@@ -112,10 +113,10 @@ class Case:
     def workspace(self, pa, weights=False):
         f = pa.attention_key_weights_workspace_size if weights else pa.attention_workspace_size
         return pa.new_workspace(f(len(self.ctx), self.q.shape[0], self.hq, self.hkv, self.d,
-                                  int(self.ctx.max()), int(self.qlens.max())))
+                                  self.bound, int(self.qlens.max())))
 
     def hints(self):
-        return dict(scale=self.scale, max_context_len=int(self.ctx.max()),
+        return dict(scale=self.scale, max_context_len=self.bound,
                     max_query_len=int(self.qlens.max()), **self.scales)
 
 
@@ -294,6 +295,54 @@ def test_mxfp4_chunks_with_room_to_stage_all_some_and_none(d, hq, hkv, share):
     out = pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, **c.hints())
     assert pa.check_error(ws, raise_on_error=False) == 0x1
     assert torch.equal(out[:61], good[:61]) and torch.equal(out[261:], good[261:])
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 4, 64), (8, 2, 64), (16, 8, 128), (24, 6, 128)])
+@pytest.mark.parametrize("qlens", [1, 2])
+@pytest.mark.parametrize("spread", [0, 12])
+def test_mxfp4_small_groups(hq, hkv, d, qlens, spread):
+    """Groups of two and four, of which two kv heads share a tile of rows where a step may have
+    enough items: many sequences under a wide bound."""
+    import paged_kv_cache_286_gb300 as pa
+    lens = [max(x, qlens) for x in EDGE] + [33, 100, 5, 17, 64] * 50
+    c = Case(lens, [1 + (i % qlens) for i in range(len(lens))], hq, hkv, d, "mxfp4", seed=hq + hkv + d, spread=spread,
+             bound=8192)
+    if spread:
+        c.q = (c.q.float() * 2.0 ** -12).bfloat16()
+    t, ctx, qsl = c.dev()
+    ws = c.workspace(pa)
+    ws[256:] = 0xFF
+    for dt in (torch.float32, torch.bfloat16):
+        out = pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, out_dtype=dt, **c.hints())
+        assert pa.check_error(ws) == 0
+        check_mx(c, out)
+    before = np.zeros((len(lens), hkv, 8192), np.float32)
+    W = torch.from_numpy(before).cuda()
+    wsw = c.workspace(pa, True)
+    out2 = pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, ctx, qsl, W, wsw, out_dtype=dt, **c.hints())
+    assert pa.check_error(wsw) == 0
+    assert torch.equal(out, out2)
+    check_weights(c, before, W.cpu().numpy(), list(range(len(lens))), 1.0)
+
+
+@pytest.mark.parametrize("head", [0, 1])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("at", [0, 37])
+def test_mxfp4_nan_block_stays_in_its_head(head, which, at):
+    import paged_kv_cache_286_gb300 as pa
+    c = Case([50, 300], [1, 1], 16, 4, 128, "mxfp4", seed=9, bound=1 << 20)  # (two heads an item)
+    t, ctx, qsl = c.dev()
+    ws = c.workspace(pa)
+    good = pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, **c.hints())
+    blk, off = int(c.tables[0, at // BS]), at % BS
+    pool = c.k if which == "k" else c.v
+    pool[blk, head, off * 64:(off + 1) * 64] = 0
+    pool[blk, head, 1024 + off * 4 + 3] = 255                       # dims 96 .. 127
+    out = pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, **c.hints())
+    mine = torch.arange(16, device="cuda") // 4 == head
+    assert torch.equal(out[1], good[1]) and torch.equal(out[0, ~mine], good[0, ~mine])
+    nan = out[0, mine].isnan()
+    assert nan.all() if which == "k" else (nan[:, 96:].all() and not nan[:, :96].any())
 
 
 def test_mxfp4_nan_block_reaches_only_the_rows_that_see_it():
