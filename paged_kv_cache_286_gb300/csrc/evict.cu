@@ -7,8 +7,8 @@
 //
 //  * select_kernel: one CTA per (sequence, kv head).  The weights are mapped to integers of the
 //    same order, which stay in shared memory; three histogram passes of 11, 11 and 10 bits find
-//    the (k - r)-th largest and how many of its equals are kept; a last pass, in order, writes the
-//    kept positions and weights.
+//    the (k - r)-th largest and how many of its equals are kept; a last pass, in order, compacts
+//    the kept positions, whose weights are then moved.
 //  * move_kernel: one CTA per (sequence, kv head, K or V, column slice).  A kept key never moves
 //    up, so rows can move in place if a batch of them is read before it is written and batches go
 //    in order: every source of a later batch lies above all that is written so far.  Positions,
@@ -62,7 +62,7 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int kSelPer = 8;  // positions of a lane in a round of the last pass
+constexpr int kSelPer = 8;  // positions of a thread in a round of the last pass
 
 // Exclusive sum over the CTA's warps of each warp's `mine` (the same in all its lanes), through
 // `slots`; *all is the total.  A barrier before it is the caller's.
@@ -86,13 +86,13 @@ template <int kThreads>
 __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a, int cached) {
   constexpr int kWarps = kThreads / 32;
   constexpr int kBins = 2048 / kThreads;  // of a thread
-  extern __shared__ uint32_t s_key[];
+  extern __shared__ __align__(16) uint32_t s_key[];
   __shared__ int hist[2048];
   __shared__ int slots[2][kWarps];
   __shared__ int s_digit, s_above;
   grid_dependency_wait();  // (the moves are not launched early: their CTAs would take SMs from this)
   const int s = blockIdx.x / a.num_kv_heads, h = blockIdx.x - s * a.num_kv_heads;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   uint32_t bits;
   const EvictSeq e = evict_seq(a, s, &bits);
   if (tid == 0 && h == 0) {
@@ -117,19 +117,25 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a, int
       const int nbits = pass == 2 ? 10 : 11;
       for (int i = tid; i < 2048; i += kThreads) hist[i] = 0;
       __syncthreads();
+      auto count = [&](uint32_t u) {
+        if ((u >> (shift + nbits)) == prefix)
+          atomicAdd(&hist[(u >> shift) & ((1u << nbits) - 1)], 1);
+      };
       if (pass == 0) {
 #pragma unroll 4
-        for (int j = tid; j < N; j += kThreads) {
+        for (int j = tid; j < e.L; j += kThreads) {
           const uint32_t u = order_key(W[j]);
           if (j < cached) s_key[j] = u;
-          atomicAdd(&hist[u >> 21], 1);
+          if (j < N) atomicAdd(&hist[u >> 21], 1);
         }
       } else {
-#pragma unroll 4
-        for (int j = tid; j < N; j += kThreads) {
-          const uint32_t u = j < cached ? s_key[j] : order_key(W[j]);
-          if ((u >> (shift + nbits)) == prefix) atomicAdd(&hist[(u >> shift) & ((1u << nbits) - 1)], 1);
+        const int quads = min(cached, N) / 4;
+        for (int j = tid; j < quads; j += kThreads) {
+          const uint4 u = reinterpret_cast<const uint4*>(s_key)[j];
+          count(u.x); count(u.y); count(u.z); count(u.w);
         }
+        for (int j = 4 * quads + tid; j < N; j += kThreads)
+          count(j < cached ? s_key[j] : order_key(W[j]));
       }
       __syncthreads();
       // the digit at which the count from the top reaches `need`: a thread sums kBins bins from
@@ -162,51 +168,89 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a, int
       need -= s_above;
     }
   }
-  // kept: order key above `prefix`, the first `need` equal to it, and the last r
-  const bool none = m == 0, all_stay = m == N;
+  // Kept: order key above `prefix`, the first `need` equal to it, and the last r.  (No weight has
+  // the order keys 0 and 2^32 - 1.)
+  const int keys = m > 0 && m < N ? min(cached, e.L) : 0;  // order keys in shared memory
+  if (m == N) prefix = 0;
+  if (m == 0) prefix = 0xffffffffu;
+  // The kept positions take the places of the order keys, which lie at or above them and were read
+  // in this round or one before, and go out from there; if the row does not fit, they go out at
+  // once.
+  const bool fits = e.L <= cached;
   int done = 0, done_eq = 0;  // kept so far; equals so far
-  for (int base = 0; base < e.L; base += kThreads * kSelPer) {
-    float w[kSelPer];
-    unsigned gt[kSelPer], eq[kSelPer];
-    int n_gt = 0, n_eq = 0;
-    const int first = base + warp * (32 * kSelPer) + lane;
+  for (int base = 0, round = 0; base < e.L; base += kThreads * kSelPer, ++round) {
+    const int j0 = base + tid * kSelPer;
+    uint32_t u[kSelPer];
+    if (j0 + kSelPer <= keys) {
 #pragma unroll
-    for (int i = 0; i < kSelPer; ++i) w[i] = first + 32 * i < e.L ? W[first + 32 * i] : 0.f;
+      for (int i = 0; i < kSelPer; i += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(s_key + j0 + i);
+        u[i] = x.x; u[i + 1] = x.y; u[i + 2] = x.z; u[i + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSelPer; ++i) u[i] = j0 + i < N ? order_key(W[j0 + i]) : 0u;
+    }
+    unsigned gt = 0, eq = 0;  // bit i: position j0 + i
 #pragma unroll
     for (int i = 0; i < kSelPer; ++i) {
-      const int j = first + 32 * i;
-      const uint32_t u = order_key(w[i]);
-      const bool in = j < N;
-      const bool g = j < e.L && (!in || all_stay || (!none && u > prefix));
-      gt[i] = __ballot_sync(0xffffffffu, g);
-      eq[i] = __ballot_sync(0xffffffffu, in && !all_stay && !none && u == prefix);
-      n_gt += __popc(gt[i]);
-      n_eq += __popc(eq[i]);
+      gt |= (u[i] > prefix ? 1u : 0u) << i;
+      eq |= (u[i] == prefix ? 1u : 0u) << i;
     }
-    int t_gt, t_eq;
-    __syncthreads();  // (the slots' readers of the round before are done)
-    // (the barriers in these: every weight of the round is read before one is written)
-    int b_gt = warps_exclusive<kWarps>(n_gt, slots[0], &t_gt);
-    int b_eq = warps_exclusive<kWarps>(n_eq, slots[1], &t_eq) + done_eq;
+    const unsigned in = (1u << max(0, min(kSelPer, N - j0))) - 1;     // to choose from
+    const unsigned there = (1u << max(0, min(kSelPer, e.L - j0))) - 1;
+    gt = (gt & in) | (there & ~in);
+    eq &= in;
+    // counts of both in one word: a round has at most 2^13 positions
+    const int mine = __popc(gt) | __popc(eq) << 16;
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    int all;
+    // (the barrier in it: every key of the round is read; slots alternate, so their readers of two
+    // rounds before are done)
+    const int before =
+        warps_exclusive<kWarps>(__shfl_sync(0xffffffffu, x, 31), slots[round & 1], &all) + x - mine;
     // place of a kept key: those kept before it, done + (above since `base`) + (equals kept
     // since `base`)
     const int eq_kept0 = min(done_eq, need);
-    const unsigned below = (1u << lane) - 1;
+    int at = done + (before & 0xffff) - eq_kept0, rank_eq = (before >> 16) + done_eq;
 #pragma unroll
     for (int i = 0; i < kSelPer; ++i) {
-      const int rank_eq = b_eq + __popc(eq[i] & below);
-      const bool is_eq = (eq[i] >> lane) & 1;
-      const bool keep = ((gt[i] >> lane) & 1) || (is_eq && rank_eq < need);
-      const int at = done + b_gt + __popc(gt[i] & below) + min(rank_eq, need) - eq_kept0;
-      if (keep) {
-        kept[at] = first + 32 * i;
-        Wd[at] = w[i];
+      const bool g = gt >> i & 1, q = eq >> i & 1;
+      if (g || (q && rank_eq < need)) {
+        const int to = at + min(rank_eq, need);
+        if (fits) s_key[to] = j0 + i;
+        else kept[to] = j0 + i;
       }
-      b_gt += __popc(gt[i]);
-      b_eq += __popc(eq[i]);
+      at += g;
+      rank_eq += q;
     }
-    done += t_gt + min(done_eq + t_eq, need) - eq_kept0;
-    done_eq += t_eq;
+    done += (all & 0xffff) + min(done_eq + (all >> 16), need) - eq_kept0;
+    done_eq += all >> 16;
+  }
+  __syncthreads();
+  // their weights: what a round reads lies at or above what it writes, and above what the rounds
+  // before have written
+  for (int base = 0; base < e.k; base += kThreads * kSelPer) {
+    float w[kSelPer];
+#pragma unroll
+    for (int i = 0; i < kSelPer; ++i) {
+      const int to = base + i * kThreads + tid;
+      if (to >= e.k) break;
+      const int j = fits ? static_cast<int>(s_key[to]) : kept[to];
+      if (fits) kept[to] = j;
+      w[i] = W[j];
+    }
+    __syncthreads();  // every weight of the round is read
+#pragma unroll
+    for (int i = 0; i < kSelPer; ++i) {
+      const int to = base + i * kThreads + tid;
+      if (to < e.k) Wd[to] = w[i];
+    }
   }
   __syncthreads();  // every weight is read
   for (int i = e.k + tid; i < e.L; i += kThreads) Wd[i] = 0.f;
