@@ -62,6 +62,12 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// Adds 1 to a word of shared memory (predicated: a branch per key costs more than the sum).
+__device__ __forceinline__ void inc_shared_if(bool yes, uint32_t at) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %0, 0;\n@p red.shared.add.u32 [%1], 1;\n}"
+               ::"r"(static_cast<uint32_t>(yes)), "r"(at) : "memory");
+}
+
 constexpr int kSelPer = 8;  // positions of a thread in a round of the last pass
 
 // Exclusive sum over the CTA's warps of each warp's `mine` (the same in all its lanes), through
@@ -108,6 +114,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a, int
               (static_cast<int64_t>(e.dst_row) * a.num_kv_heads + h) * a.max_keys;
   const int N = e.L - e.r;   // the keys to choose from
   const int m = e.k - e.r;   // how many of them stay
+  const uint32_t bins = smem_u32(hist);
   uint32_t prefix = 0;       // the m-th largest order key, digit by digit
   int need = m;              // how many keys with the prefix so far are kept
   if (m > 0 && m < N) {
@@ -118,15 +125,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a, int
       for (int i = tid; i < 2048; i += kThreads) hist[i] = 0;
       __syncthreads();
       auto count = [&](uint32_t u) {
-        if ((u >> (shift + nbits)) == prefix)
-          atomicAdd(&hist[(u >> shift) & ((1u << nbits) - 1)], 1);
+        inc_shared_if((u >> (shift + nbits)) == prefix,
+                      bins + 4 * ((u >> shift) & ((1u << nbits) - 1)));
       };
       if (pass == 0) {
 #pragma unroll 4
         for (int j = tid; j < e.L; j += kThreads) {
           const uint32_t u = order_key(W[j]);
           if (j < cached) s_key[j] = u;
-          if (j < N) atomicAdd(&hist[u >> 21], 1);
+          inc_shared_if(j < N, bins + 4 * (u >> 21));
         }
       } else {
         const int quads = min(cached, N) / 4;
@@ -217,17 +224,14 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a, int
     // place of a kept key: those kept before it, done + (above since `base`) + (equals kept
     // since `base`)
     const int eq_kept0 = min(done_eq, need);
-    int at = done + (before & 0xffff) - eq_kept0, rank_eq = (before >> 16) + done_eq;
-#pragma unroll
-    for (int i = 0; i < kSelPer; ++i) {
-      const bool g = gt >> i & 1, q = eq >> i & 1;
-      if (g || (q && rank_eq < need)) {
-        const int to = at + min(rank_eq, need);
-        if (fits) s_key[to] = j0 + i;
-        else kept[to] = j0 + i;
-      }
-      at += g;
-      rank_eq += q;
+    const int rank_eq = (before >> 16) + done_eq;
+    int to = done + (before & 0xffff) + min(rank_eq, need) - eq_kept0;
+    for (int more = __popc(eq) - max(0, need - rank_eq); more > 0; --more)
+      eq &= ~(0x80000000u >> __clz(eq));  // (equals beyond `need`)
+    for (unsigned stay = gt | eq; stay; stay &= stay - 1, ++to) {
+      const int j = j0 + __ffs(stay) - 1;
+      if (fits) s_key[to] = j;
+      else kept[to] = j;
     }
     done += (all & 0xffff) + min(done_eq + (all >> 16), need) - eq_kept0;
     done_eq += all >> 16;
