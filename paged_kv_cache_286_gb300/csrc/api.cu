@@ -667,11 +667,10 @@ pa_status pa_attention_key_weights(
   a.decay = decay;
   a.wait_ns = g_wait_ns;
   a.skip_copy = g_skip_copy;
-  // Long runs over bf16 keys go to the tensor-core kernel if their key chunks, one to a CTA, fill at
+  // Long runs go to the tensor-core kernel if their key chunks, one to a CTA, fill at
   // least half the SMs; with fewer, four CTAs to a chunk of the other kernel end sooner.
   pa::PoolMaps maps;
-  bool tc = a.k_pass && cache->cache_dtype == PA_BF16 &&
-            pa::prefill_geometry(num_q_heads, num_kv_heads);
+  bool tc = a.k_pass && pa::prefill_geometry(num_q_heads, num_kv_heads);
   if (tc) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -680,9 +679,11 @@ pa_status pa_attention_key_weights(
     tc = 2 * int64_t(num_kv_heads) * ((max_context_len - 1) / pa::kKeyWeightsTcKeys + 1) >= sms;
   }
   if (tc) {
-    st = head_dim == 128 ? encode_pool_tile_map(&maps.k4, k_cache, *cache)
-                         : encode_pool_map(&maps.k2, k_cache, *cache);
-    if (st != PA_OK) return st;
+    if (cache->cache_dtype == PA_BF16) {
+      st = head_dim == 128 ? encode_pool_tile_map(&maps.k4, k_cache, *cache)
+                           : encode_pool_map(&maps.k2, k_cache, *cache);
+      if (st != PA_OK) return st;
+    }
     if ((st = encode_q_map(&maps.q3, q, num_q_tokens, num_q_heads, head_dim,
                            num_q_heads / num_kv_heads)) != PA_OK)
       return st;

@@ -1,4 +1,4 @@
-// Accumulated key weights of long query runs over bf16 keys, on the tensor cores (tcgen05).
+// Accumulated key weights of long query runs on the tensor cores (tcgen05).
 //
 // W[j] <- decay * W[j] + sum over the rows (query token, q head of the group) that see key j of
 // 2^(s_j - lse_row), as in key_weights.cu, for runs whose scores the attention did not keep.
@@ -10,8 +10,14 @@
 //  * A CTA holds an item's keys (256 of one kv head, 64 KiB, two accumulators) while the rows pass:
 //    128 / G tokens x G heads a tile, one 3-D TMA box per 64 columns, four tiles in flight, two pairs
 //    of accumulators.  Warp 0 copies, warp 1 issues the MMAs, warps 2-17 read the accumulators.
+//  * E4M3 and MXFP4 keys become bf16 (exact: four significant bits and two) on their way in, by the
+//    warps 2-17, once per item; copied K tiles cost less, but a conversion beforehand would write
+//    and read four or eight times the bytes.
 //  * A score costs the epilogue an FMA, a 2^x and an add; the 2^x bound it from below (32 a cycle
-//    and SM: 0.5 us a tile of 256 x 128), the MMAs take about as long.
+//    and SM: 0.5 us a tile of 256 x 128), the MMAs take about as long.  Two runs of 2,048 tokens
+//    x 32 heads after 6,144 (8 kv heads of 128): 338 us for bf16 keys, 712 TFLOP/s, 349 us for E4M3
+//    and 350 us for MXFP4, where the mma.sync kernel took 1,280; one run of 512 x 32 in 2,560 keys
+//    beside one of 512 x 32 in 512 31 us.
 //  * Every wait is bounded; when one runs out the CTA records PA_DEVERR_TIMEOUT, stops, lets its
 //    copies and MMAs finish (bounded again) and frees its tensor memory.
 #include <math_constants.h>
@@ -21,6 +27,7 @@
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
+#include "pool_keys.cuh"
 
 namespace pa {
 
@@ -73,7 +80,7 @@ __device__ __forceinline__ TcItem tc_item(const KeyWeightsArgs& a, int64_t item,
   return it;
 }
 
-template <int D>
+template <Pool kPool, int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     key_weights_tc_kernel(const __grid_constant__ CUtensorMap qmap,
                           const __grid_constant__ CUtensorMap kmap, const KeyWeightsArgs a) {
@@ -87,7 +94,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kTcKStages; ++i) {
-      mbar_init(&ctl.k_full[i], 1);
+      mbar_init(&ctl.k_full[i], kPool == Pool::kBf16 ? 1 : kTcEpilogue);
       mbar_init(&ctl.k_empty[i], 1);
     }
     for (int i = 0; i < kTcQStages; ++i) {
@@ -104,7 +111,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     ctl.abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&qmap);
-    prefetch_tensormap(&kmap);
+    if (kPool == Pool::kBf16) prefetch_tensormap(&kmap);
   }
   if (warp == 1) tmem_alloc(&ctl.tmem_base, kTcCols);
   tc_fence_before();
@@ -131,26 +138,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ---------------------------------------------------------------- producer (TMA)
     for (int64_t item = blockIdx.x; ok && item < total; item += gridDim.x, ++kc) {
       const TcItem I = tc_item(a, item, tpt);
-      const uint32_t ks = kc % kTcKStages;
-      const int jb = I.base / kBlockSize + lane;  // this lane's block of the keys
-      int phys = -1;
-      if (lane < kTcKeys / kBlockSize && jb * kBlockSize < I.L) {
-        phys = __ldg(a.block_tables + static_cast<int64_t>(I.s) * a.max_blocks_per_seq + jb);
-        if (phys >= a.num_blocks) phys = -1;  // (flagged by the attention)
-      }
-      if (!(ok = wait(&ctl.k_empty[ks], ((kc / kTcKStages) & 1u) ^ 1u))) break;
-      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, phys >= 0)) * (kBlockSize * D * 2);
-      if (lane == 0) {
-        if (bytes) mbar_arrive_expect_tx(&ctl.k_full[ks], bytes);
-        else mbar_arrive(&ctl.k_full[ks]);
-      }
-      __syncwarp();
-      // test hook: the first item's first copy is left out while its bytes are expected
-      if (phys >= 0 && !(a.skip_copy && item == 0 && lane == 0)) {
-        uint8_t* dst = smem + L::kK + ks * 2 * L::kTile + lane * (kBlockSize * D * 2);
-        const int group = (phys * a.num_kv_heads + I.h) * 2;  // its first group of 8 pool rows
-        if constexpr (D == 128) tma_load_4d(dst, &kmap, 0, 0, 0, group, &ctl.k_full[ks]);
-        else tma_load_2d(dst, &kmap, 0, group * 8, &ctl.k_full[ks]);
+      if constexpr (kPool == Pool::kBf16) {
+        const uint32_t ks = kc % kTcKStages;
+        const int jb = I.base / kBlockSize + lane;  // this lane's block of the keys
+        int phys = -1;
+        if (lane < kTcKeys / kBlockSize && jb * kBlockSize < I.L) {
+          phys = __ldg(a.block_tables + static_cast<int64_t>(I.s) * a.max_blocks_per_seq + jb);
+          if (phys >= a.num_blocks) phys = -1;  // (flagged by the attention)
+        }
+        if (!(ok = wait(&ctl.k_empty[ks], ((kc / kTcKStages) & 1u) ^ 1u))) break;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, phys >= 0)) * (kBlockSize * D * 2);
+        if (lane == 0) {
+          if (bytes) mbar_arrive_expect_tx(&ctl.k_full[ks], bytes);
+          else mbar_arrive(&ctl.k_full[ks]);
+        }
+        __syncwarp();
+        // test hook: the first item's first copy is left out while its bytes are expected
+        if (phys >= 0 && !(a.skip_copy && item == 0 && lane == 0)) {
+          uint8_t* dst = smem + L::kK + ks * 2 * L::kTile + lane * (kBlockSize * D * 2);
+          const int group = (phys * a.num_kv_heads + I.h) * 2;  // its first group of 8 pool rows
+          if constexpr (D == 128) tma_load_4d(dst, &kmap, 0, 0, 0, group, &ctl.k_full[ks]);
+          else tma_load_2d(dst, &kmap, 0, group * 8, &ctl.k_full[ks]);
+        }
       }
       for (int t = 0; t < I.tiles; ++t, ++qc) {
         const uint32_t qs = qc % kTcQStages;
@@ -167,7 +176,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
     // the latest fill of each stage is the only one that can still be in flight
-    for (uint32_t g = kc > kTcKStages ? kc - kTcKStages : 0; g < kc + (ok ? 0 : 1); ++g)
+    for (uint32_t g = kc > kTcKStages ? kc - kTcKStages : 0;
+         kPool == Pool::kBf16 && g < kc + (ok ? 0 : 1); ++g)
       mbar_wait(&ctl.k_full[g % kTcKStages], (g / kTcKStages) & 1u, a.wait_ns);
     for (uint32_t g = qc > kTcQStages ? qc - kTcQStages : 0; g < qc; ++g)
       mbar_wait(&ctl.q_full[g % kTcQStages], (g / kTcQStages) & 1u, a.wait_ns);
@@ -228,6 +238,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                    : -CUDART_INF_F;
       };
       float next0 = lse_of(0, tok_0, g_0), next1 = lse_of(0, tok_1, g_1);
+      if constexpr (kPool != Pool::kBf16) {
+        // the item's keys, converted by these warps: 16-byte pieces (8 dims) of the K tiles' layout
+        constexpr int kEach = kTcKeys * (D / 8) / (32 * kTcEpilogue);
+        const uint32_t ks = kc % kTcKStages;
+        uint32_t w[kEach][4];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const int piece = (i * kTcEpilogue + e) * 32 + lane, kk = piece / (D / 8), c = piece % (D / 8);
+          w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
+          if (I.base + kk >= I.L) continue;
+          const int phys = __ldg(a.block_tables + static_cast<int64_t>(I.s) * a.max_blocks_per_seq +
+                                 (I.base + kk) / kBlockSize);
+          if (phys < 0 || phys >= a.num_blocks) continue;  // (flagged by the attention)
+          load_dims<kPool, D>(a.k_cache, static_cast<int64_t>(phys) * a.num_kv_heads + I.h,
+                              kk % kBlockSize, c >> 2, c & 3, w[i]);
+        }
+        if (!(ok = wait(&ctl.k_empty[ks], ((kc / kTcKStages) & 1u) ^ 1u))) break;
+        const uint32_t base = smem_u32(smem + L::kK + ks * 2 * L::kTile);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const int piece = (i * kTcEpilogue + e) * 32 + lane, kk = piece / (D / 8), c = piece % (D / 8);
+          st_shared_v4(base + (kk >> 3) * (D * 16) + (c >> 3) * 1024 + (kk & 7) * 128 +
+                           (((c & 7) ^ (kk & 7)) << 4),
+                       w[i][0], w[i][1], w[i][2], w[i][3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.k_full[ks]);
+      }
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
       for (int t = 0; t < I.tiles; ++t, ++qc) {
         const uint32_t b = qc % kTcBufs;
@@ -297,9 +336,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, kTcCols);
 }
 
-template <int D>
+template <Pool kPool, int D>
 cudaError_t run_tc(const KeyWeightsArgs& a, const PoolMaps& maps, cudaStream_t stream) {
-  auto kern = key_weights_tc_kernel<D>;
+  auto kern = key_weights_tc_kernel<kPool, D>;
   LaunchInfo li;
   cudaError_t e = launch_info(kern, kTcThreads, TcLayout<D>::kSmem, &li);
   if (e != cudaSuccess) return e;
@@ -314,7 +353,12 @@ cudaError_t run_tc(const KeyWeightsArgs& a, const PoolMaps& maps, cudaStream_t s
 
 cudaError_t launch_key_weights_tc(const KeyWeightsArgs& a, const PoolMaps& maps,
                                   cudaStream_t stream) {
-  return a.head_dim == 128 ? run_tc<128>(a, maps, stream) : run_tc<64>(a, maps, stream);
+  if (a.cache_dtype == PA_FP8_E4M3) return run_tc<Pool::kE4m3, 128>(a, maps, stream);
+  if (a.cache_dtype == PA_MXFP4)
+    return a.head_dim == 128 ? run_tc<Pool::kMx, 128>(a, maps, stream)
+                             : run_tc<Pool::kMx, 64>(a, maps, stream);
+  return a.head_dim == 128 ? run_tc<Pool::kBf16, 128>(a, maps, stream)
+                           : run_tc<Pool::kBf16, 64>(a, maps, stream);
 }
 
 }  // namespace pa

@@ -20,12 +20,6 @@ struct Mx {
   static constexpr int kCodeBytes = kBlockSize * kRowBytes;
   static constexpr int kTileBytes = kCodeBytes + kBlockSize * kBlocks;
 };
-inline int mx_tile_bytes(int head_dim) { return head_dim * 17 / 2; }
-
-// 16-bit word of a row that holds dims d .. d + 3 (d a multiple of 4).
-__host__ __device__ constexpr int mx_word_of(int d, int blocks) {
-  return ((d & 31) >> 2) * blocks + (d >> 5);
-}
 
 // Eight E2M1 codes to four exact f16 pairs, byte i (low nibble in the low half) to out[i].
 __device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t w, uint32_t (&out)[4]) {

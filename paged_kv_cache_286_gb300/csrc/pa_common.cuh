@@ -191,10 +191,6 @@ __device__ __forceinline__ void st_f32x2_hint(float* p, float x, float y, uint64
                "l"(policy)
                : "memory");
 }
-__device__ __forceinline__ void st_f32_hint(float* p, float x, uint64_t policy) {
-  asm volatile("st.global.L2::cache_hint.f32 [%0], %1, %2;" ::"l"(p), "f"(x), "l"(policy)
-               : "memory");
-}
 
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");

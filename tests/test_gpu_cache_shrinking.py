@@ -467,6 +467,33 @@ def test_key_weights_of_chunks_on_the_tensor_cores(d, hq, hkv):
     assert torch.equal(W2[3, :, 320:336].cpu(), torch.from_numpy(before[3, :, 320:336] * np.float32(0.5)))
 
 
+@pytest.mark.parametrize("kind,d,hq,hkv", [("e4m3", 128, 16, 16), ("e4m3", 128, 64, 16), ("mxfp4", 128, 40, 20),
+                                           ("mxfp4", 64, 32, 16), ("mxfp4", 128, 128, 16)])
+def test_key_weights_of_chunks_over_small_pools_on_the_tensor_cores(kind, d, hq, hkv):
+    """As above; the keys are converted on their way in."""
+    import paged_kv_cache_286_gb300 as pa
+    qlens, ctx = [200, 1, 33, 70, 0, 129, 300], [1300, 500, 33, 900, 44, 641, 2000]
+    c = Case(ctx, qlens, hq, hkv, d, kind, seed=d + hq)
+    t, ctx, qsl = c.dev()
+    before = np.random.default_rng(2).random((7, hkv, 2003)).astype(np.float32)
+    W = torch.from_numpy(before).cuda()
+    ws = c.workspace(pa, True)
+    ws[256:] = 0xFF
+    pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, ctx, qsl, W, ws, decay=0.5, **c.hints())
+    assert pa.check_error(ws) == 0
+    check_weights(c, before, W.cpu().numpy(), list(range(7)), 0.5)
+    W2 = torch.from_numpy(before).cuda()
+    pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, ctx, qsl, W2, ws, decay=0.5, **c.hints())
+    assert torch.equal(W, W2)
+    t[3, 20] = 10 ** 6
+    W2 = torch.from_numpy(before).cuda()
+    pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, ctx, qsl, W2, ws, decay=0.5, **c.hints())
+    assert pa.check_error(ws, raise_on_error=False) == 0x1
+    keep = [0, 1, 2, 4, 5, 6]
+    assert torch.equal(W[keep], W2[keep])
+    assert torch.equal(W2[3, :, 320:336].cpu(), torch.from_numpy(before[3, :, 320:336] * np.float32(0.5)))
+
+
 def test_key_weights_wait_that_expires_reports_a_timeout():
     import paged_kv_cache_286_gb300 as pa
     c = Case([1300, 500], [200, 1], 16, 16, 64, "bf16", seed=3)
