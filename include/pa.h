@@ -147,7 +147,9 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const pa_cache_desc* cach
                          cudaStream_t stream);
 
 /* Workspace bytes pa_attention needs for a step of this shape (host-only, no device call).
- * max_context_len / max_query_len are upper bounds of context_lens[s] and n_s. */
+ * max_context_len / max_query_len are upper bounds of context_lens[s] and n_s.  With runs of more
+ * than 32 (token x q head) rows up to 256 MiB of it are for the bf16 copies that MXFP4 pools use
+ * (see pa_attention); steps over other pools need not have them. */
 size_t pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_tokens, int32_t num_q_heads,
                                    int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                    int32_t max_context_len, int32_t max_query_len);
@@ -171,8 +173,11 @@ size_t pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_tokens, int32
  * 128 or 64 or an E4M3 pool of head_dim 128 and query runs of more than 16 tokens or more than
  * 16 (token x q head) rows, the tensor-core prefill tiles on the part of the SMs the plan gives
  * them, the split-KV kernel on the rest, and the merge of split sequences.
- * MXFP4 pools have their own split-KV kernel, which takes runs of any length in tiles of up to 32
- * rows.
+ * MXFP4 pools have their own split-KV kernel for runs of up to 32 (token x q head) rows.  The
+ * sequences of longer runs are written out as bf16 into the end of the workspace and go to the
+ * prefill tiles, if the heads allow those (128 divisible by the group, at most 8); a workspace that
+ * holds the split-KV part but not all of that copy is accepted, and the split-KV kernel then also
+ * takes the runs for whose sequences it has no room.
  * Work enqueued on `stream` after the call sees all of it complete.  The call records no event
  * and creates no stream, so it can be captured into a CUDA graph like any kernel launch. */
 pa_status pa_attention(const void* q, int32_t num_q_tokens, const void* k_cache,
@@ -184,7 +189,9 @@ pa_status pa_attention(const void* q, int32_t num_q_tokens, const void* k_cache,
                        void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes,
                        cudaStream_t stream);
 
-/* Workspace bytes pa_attention_key_weights needs for a step of this shape (host-only). */
+/* Workspace bytes pa_attention_key_weights needs for a step of this shape (host-only): what
+ * pa_attention needs, the rows' log-sum-exps, and, where they are at most 1 GiB, the scores of the
+ * decode tokens and short runs (with more, those runs' keys are read a second time). */
 size_t pa_attention_key_weights_workspace_size(int32_t num_seqs, int32_t num_q_tokens,
                                                int32_t num_q_heads, int32_t num_kv_heads,
                                                int32_t head_dim, int32_t block_size,
@@ -267,8 +274,9 @@ pa_status pa_evict_keys(void* k_cache, void* v_cache, const pa_cache_desc* cache
  * path where an allocation could stall the device.  They can still pass inputs and outputs but
  * not a workspace, so this call uses a scratch array built into the library instead:
  * PA_NOALLOC_SCRATCH_BYTES per device, held by every GPU that loads the library until the
- * process exits.  A step whose pa_attention_workspace_size exceeds it is rejected with
- * PA_ERR_INVALID_ARG and a message; use pa_attention with a workspace for larger steps.
+ * process exits.  A step whose pa_attention_workspace_size, less its part for MXFP4 copies, exceeds
+ * it is rejected with PA_ERR_INVALID_ARG and a message; use pa_attention with a workspace for larger
+ * steps.
  *   Arguments are those of pa_attention without workspace/workspace_bytes, plus
  *   error_word    optional DEVICE pointer (may be NULL) that receives, asynchronously on
  *                 `stream`, this call's PA_DEVERR_* bits (0 for a step with nothing to do).  It
@@ -335,8 +343,8 @@ void pa_set_wait_limit_ns(uint64_t ns);
  * launches (the first copy of the first work item claimed) while that copy's barrier still
  * expects the bytes, so that the bounded waits on it expire and the call ends with
  * PA_ERR_TIMEOUT without any fault: the expiry and drain paths of the kernels can be exercised
- * on a real GPU.  (The split-KV kernel of MXFP4 pools has no wait that could run out and ignores
- * the hook.) */
+ * on a real GPU.  pa_attention_key_weights' tensor-core kernel does the same over bf16 pools.  (The
+ * split-KV kernel of MXFP4 pools has no wait that could run out and ignores the hook.) */
 void pa_test_skip_one_copy(int32_t enable);
 
 /* Self-test of the bounded wait: one thread waits, for limit_ns (in (0, 10 s]), on an mbarrier

@@ -256,9 +256,10 @@ KeyWeightsLayout key_weights_layout(int32_t S, int32_t T, int32_t Hq, int32_t Hk
   // (they are bounded by the longest context, not by the keys there are): K is read again then.
   const int64_t G = Hkv > 0 ? Hq / Hkv : 1;
   w.score_rows = static_cast<int32_t>(std::min<int64_t>(kDecodeMaxRows, std::max(max_q, 1) * G));
-  w.score_stride = (std::max(max_ctx, 1) + kBlockSize - 1) / kBlockSize * kBlockSize;
-  const double bytes = 4.0 * std::max(S, 0) * std::max(Hkv, 0) * w.score_rows * w.score_stride;
+  const int64_t stride = (std::max(max_ctx, 1) + int64_t(kBlockSize) - 1) / kBlockSize * kBlockSize;
+  const double bytes = 4.0 * std::max(S, 0) * std::max(Hkv, 0) * w.score_rows * stride;
   if (bytes > double(1 << 30)) w.score_rows = 0;
+  w.score_stride = w.score_rows ? static_cast<int32_t>(stride) : 0;
   w.scores = off;
   off = up(off + sizeof(float) * size_t(std::max(S, 0)) * size_t(std::max(Hkv, 0)) *
                      size_t(w.score_rows) * size_t(w.score_stride));
@@ -667,8 +668,10 @@ pa_status pa_attention_key_weights(
   a.decay = decay;
   a.wait_ns = g_wait_ns;
   a.skip_copy = g_skip_copy;
-  // Long runs go to the tensor-core kernel if their key chunks, one to a CTA, fill at
-  // least half the SMs; with fewer, four CTAs to a chunk of the other kernel end sooner.
+  // Long runs go to the tensor-core kernel if their key chunks, one to a CTA, fill at least half the
+  // SMs; with fewer, four CTAs to a chunk of the other kernel end sooner.  (8 kv heads, E4M3, 32 q
+  // heads: a run of 512 tokens in 1,280 keys, 40 chunks, 31 us here and 29 there; in 2,560 keys 32
+  // and 67; eight runs of 100 tokens in 300 keys 16 and 33.)
   pa::PoolMaps maps;
   bool tc = a.k_pass && pa::prefill_geometry(num_q_heads, num_kv_heads);
   if (tc) {
@@ -676,7 +679,13 @@ pa_status pa_attention_key_weights(
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_fail(e, "pa_attention_key_weights");
-    tc = 2 * int64_t(num_kv_heads) * ((max_context_len - 1) / pa::kKeyWeightsTcKeys + 1) >= sms;
+    // runs longer than a token that the step has at least
+    const int64_t runs = max_query_len == 1
+        ? num_seqs
+        : std::max<int64_t>(1, (int64_t(num_q_tokens) - num_seqs + max_query_len - 2) /
+                                   (max_query_len - 1));
+    tc = 2 * std::min<int64_t>(runs, num_seqs) * num_kv_heads *
+             ((max_context_len - 1) / pa::kKeyWeightsTcKeys + 1) >= sms;
   }
   if (tc) {
     if (cache->cache_dtype == PA_BF16) {

@@ -9,11 +9,14 @@
 //    same order, which stay in shared memory; three histogram passes of 11, 11 and 10 bits find
 //    the (k - r)-th largest and how many of its equals are kept; a last pass, in order, compacts
 //    the kept positions, whose weights are then moved.
+//    Instructions bound it, some 100 per 32 keys, then the latency of its eleven barriers: 16 x 8
+//    rows of 32,768 weights 24 us, 64 x 32 rows of 2,300 on average 37 us.
 //  * move_kernel: one CTA per (sequence, kv head, K or V, column slice).  A kept key never moves
 //    up, so rows can move in place if a batch of them is read before it is written and batches go
 //    in order: every source of a later batch lies above all that is written so far.  Positions,
 //    table entries and rows are loads that wait on one another; they run two, one and no batches
-//    ahead.
+//    ahead.  HBM bounds it: 64 x 32 x 1,001 rows of 256 bytes, K and V, 308 us (2.1 GB read and
+//    written, 6.8 TB/s); 16 x 8 x 2,048 rows 45 us (5.9 TB/s).
 #include <math_constants.h>
 
 #include <algorithm>

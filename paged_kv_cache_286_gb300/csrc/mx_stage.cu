@@ -5,7 +5,9 @@
 // A chunk reads each of its sequence's tiles once for every 128 rows of queries, so converting
 // them once (2 KiB written per 544 bytes read, the copy of a 2,560-key context for 8 kv heads
 // 10 MB) costs less than converting them in every tile; and the MMAs cannot take the codes as they
-// are: V's scales change along the keys, the dimension that P V sums over.
+// are: V's scales change along the keys, the dimension that P V sums over.  Measured: that copy 6.7
+// us, the plan before it 2.8; a run of 512 x 32 heads over it beside 16 decodes 74 us in all, where
+// the split-KV kernel alone took 327.
 #include <algorithm>
 
 #include "decode_items.cuh"

@@ -325,6 +325,91 @@ def test_mxfp4_small_groups(hq, hkv, d, qlens, spread):
     check_weights(c, before, W.cpu().numpy(), list(range(len(lens))), 1.0)
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (16, 8, 64)])
+def test_mxfp4_partitions_cut_to_even_rounds(hq, hkv, d):
+    """Contexts of up to 3,000 keys under a bound for which the partitions are longer than 128 blocks."""
+    import paged_kv_cache_286_gb300 as pa
+    lens = [3000, 1, 2353, 2352, 640, 17, 2999, 100, 16, 15, 2000, 33, 1040, 48, 2, 2368]
+    c = Case(lens, [1] * 16, hq, hkv, d, "mxfp4", seed=d, bound=32768)
+    t, ctx, qsl = c.dev()
+    ws = c.workspace(pa)
+    ws[256:] = 0xFF
+    out = pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, **c.hints())
+    assert pa.check_error(ws) == 0
+    check_mx(c, out)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_mxfp4_without_a_workspace(d):
+    """The built-in scratch: a step with a chunk, which is not staged there."""
+    import paged_kv_cache_286_gb300 as pa
+    qlens, ctx = [40, 1, 2], [300, 900, 50]
+    c = Case(ctx, qlens, 8, 2, d, "mxfp4", seed=17)
+    t, ctx, qsl = c.dev()
+    L, q = pa.library(), c.q.cuda()
+    word = torch.full((1,), 7, dtype=torch.int32, device="cuda")
+    out = torch.empty(43, 8, d, device="cuda")
+    desc = pa.cache_desc(c.k)
+    for _ in range(2):
+        pa._lib.check(L.pa_attention_noalloc(
+            pa._ptr(q), 43, pa._ptr(c.k), pa._ptr(c.v), ctypes.byref(desc), pa._ptr(t), t.size(1), pa._ptr(ctx),
+            pa._ptr(qsl), 3, c.bound, 40, 8, 2, d, c.scale, pa._ptr(out), 2, pa._ptr(word), None))
+        torch.cuda.synchronize()
+        assert word.item() == 0
+        check_mx(c, out)
+
+
+def test_mxfp4_steps_in_graphs_on_two_streams():
+    """Two captured steps (append, attention with a staged chunk, key weights, eviction) with
+    workspaces of their own, replayed at once, give what the same calls give one after the other."""
+    import paged_kv_cache_286_gb300 as pa
+    cases = [Case([500, 900, 77], [60, 1, 3], 8, 2, 128, "mxfp4", seed=s) for s in (1, 2)]
+
+    def state(c):
+        t, ctx, qsl = c.dev()
+        slots = torch.from_numpy(np.concatenate([c.tables[s][:1] * BS + np.arange(3) for s in range(3)]).astype(np.int64)).cuda()
+        W = torch.zeros(3, 2, 900, device="cuda")
+        keep = torch.tensor([200, 333, 77], dtype=torch.int32, device="cuda")
+        kv = [torch.randn(9, 2, 128, generator=torch.Generator().manual_seed(c.hq + i)).bfloat16().cuda() for i in range(2)]
+        ws = c.workspace(pa, True)
+        ws[256:] = 0xFF
+        return dict(c=c, t=t, ctx=ctx, qsl=qsl, slots=slots, W=W, keep=keep, kv=kv, ws=ws, k=c.k.clone(), v=c.v.clone(),
+                    q=c.q.cuda(), out=torch.empty(64, 8, 128, device="cuda"),
+                    kept=torch.empty(3, 2, 400, dtype=torch.int32, device="cuda"),
+                    lens=torch.empty(3, dtype=torch.int32, device="cuda"))
+
+    def run(s):
+        c = s["c"]
+        pa.cache_append(*s["kv"], s["slots"], s["k"], s["v"], s["ws"])
+        pa.attention_key_weights(s["q"], s["k"], s["v"], s["t"], s["ctx"], s["qsl"], s["W"], s["ws"], out=s["out"],
+                                 **c.hints())
+        pa.evict_keys(s["k"], s["v"], s["t"], s["ctx"], s["keep"], s["W"], s["ws"], max_context_len=900,
+                      max_keep_len=400, recent=10, kept=s["kept"], new_lens=s["lens"])
+
+    want = [state(c) for c in cases]
+    for s in want:
+        for _ in range(2):
+            run(s)
+    torch.cuda.synchronize()
+    got = [state(c) for c in cases]
+    streams, graphs = [torch.cuda.Stream() for _ in cases], []
+    for s, st in zip(got, streams):
+        st.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            run(s)
+        graphs.append(graph)
+    for _ in range(2):
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert pa.check_error(b["ws"]) == 0
+        for x in ("out", "W", "kept", "lens", "k", "v"):
+            assert torch.equal(a[x], b[x]), x
+
+
 @pytest.mark.parametrize("head", [0, 1])
 @pytest.mark.parametrize("which", ["k", "v"])
 @pytest.mark.parametrize("at", [0, 37])
@@ -657,6 +742,25 @@ def test_evict_long_rows_and_default_rows(ctx, keep, hkv, weights):
         assert np.array_equal(Wt.cpu().numpy(), args[4], equal_nan=True)
         assert np.array_equal(tile_rows(k, "bf16", 64), args[2])
         assert np.array_equal(tile_rows(v, "bf16", 64), args[3])
+
+
+def test_evict_of_empty_sequences_and_to_nothing():
+    import paged_kv_cache_286_gb300 as pa
+    c = Case([40, 16, 50], [1] * 3, 2, 2, 64, "bf16", seed=14)
+    t, _, _ = c.dev()
+    ctx = torch.tensor([40, 0, 50], dtype=torch.int32, device="cuda")
+    keep = torch.tensor([0, 9, 0], dtype=torch.int32, device="cuda")
+    W = torch.rand(3, 2, 64, device="cuda")
+    w0, k0 = W.cpu().numpy().copy(), tile_rows(c.k, "bf16", 64)
+    ws = pa.new_workspace(256)
+    for most in (8, 0):
+        kept, lens = pa.evict_keys(c.k, c.v, t, ctx, keep, W, ws, max_context_len=64, max_keep_len=most, recent=4)
+        assert pa.check_error(ws) == 0
+        assert lens.tolist() == [0, 0, 0] and kept.shape == (3, 2, most) and (kept == -1).all()
+        got = W.cpu().numpy()
+        assert (got[0, :, :40] == 0).all() and (got[2, :, :50] == 0).all()
+        assert np.array_equal(got[0, :, 40:], w0[0, :, 40:]) and np.array_equal(got[1], w0[1])
+        assert np.array_equal(tile_rows(c.k, "bf16", 64), k0)
 
 
 def test_evict_leaves_bad_sequences_as_they_are():
