@@ -388,10 +388,14 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   // A pass over short rows costs mostly what every warp does once (bins, scans), so few warps a CTA
-  // and many CTAs; long rows, or few, want the CTA's time short.
-  e = a.max_context_len <= 4096 || pairs >= 8 * int64_t(sms) ? run_select<128>(a, pairs, stream)
-      : a.max_context_len <= 8192                            ? run_select<512>(a, pairs, stream)
-                                                             : run_select<1024>(a, pairs, stream);
+  // and many CTAs; few rows want the CTA's time short, and of long ones shared memory holds few.
+  // With 128, 512 and 1,024 threads: 2,048 rows of 4,096 weights 49, 57 and 106 us, of 16,384 227,
+  // 133 and 197; 1,216 of 32,768 565, 232 and 180; 128 rows of 4,096 14, 10 and 10, of 16,384 33,
+  // 17 and 14.
+  const bool few = pairs <= 2 * int64_t(sms);
+  e = a.max_context_len > (few ? 4096 : 16384)   ? run_select<1024>(a, pairs, stream)
+      : few || a.max_context_len > 4096          ? run_select<512>(a, pairs, stream)
+                                                 : run_select<128>(a, pairs, stream);
   if (e != cudaSuccess || a.max_keep_len == 0) return e;
   // Batches of a (sequence, kv head, K or V) go one after another, but columns are independent:
   // few of them are cut into slices of at least 64 bytes, while they all are resident at once.

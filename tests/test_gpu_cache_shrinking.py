@@ -342,6 +342,7 @@ def test_mxfp4_partitions_cut_to_even_rounds(hq, hkv, d):
 @pytest.mark.parametrize("d", [64, 128])
 def test_mxfp4_without_a_workspace(d):
     """The built-in scratch: a step with a chunk, which is not staged there."""
+    import ctypes
     import paged_kv_cache_286_gb300 as pa
     qlens, ctx = [40, 1, 2], [300, 900, 50]
     c = Case(ctx, qlens, 8, 2, d, "mxfp4", seed=17)
@@ -742,6 +743,29 @@ def test_evict_long_rows_and_default_rows(ctx, keep, hkv, weights):
         assert np.array_equal(Wt.cpu().numpy(), args[4], equal_nan=True)
         assert np.array_equal(tile_rows(k, "bf16", 64), args[2])
         assert np.array_equal(tile_rows(v, "bf16", 64), args[3])
+
+
+@pytest.mark.parametrize("weights", sorted(WEIGHTS))
+@pytest.mark.parametrize("bound", [300, 5000, 20000])
+def test_evict_of_many_rows(weights, bound):
+    """More rows than fill the GPU, under bounds that choose each width of the selection."""
+    import paged_kv_cache_286_gb300 as pa
+    rng = np.random.default_rng(31)
+    ctx = rng.integers(1, 301, 160)
+    keep = np.maximum(1, (ctx * rng.random(160)).astype(np.int32)).astype(np.int32)
+    c = Case(ctx, [1] * 160, 2, 2, 64, "bf16", seed=15)
+    W0 = WEIGHTS[weights](rng, (160, 2, bound)).astype(np.float32)
+    rows = list(range(160))
+    want = evict_reference(c, W0, c.ctx, keep, 7, 300, c.tables, rows, rows)
+    Wt, (t, lens, _) = torch.from_numpy(W0).cuda(), c.dev()
+    t = torch.nn.functional.pad(t, (0, -(-bound // BS) - t.size(1)), value=-1) if bound > 300 else t
+    ws = pa.new_workspace(256)
+    kept, new = pa.evict_keys(c.k, c.v, t, lens, torch.from_numpy(keep).cuda(), Wt, ws, max_context_len=bound,
+                              max_keep_len=300, recent=7)
+    assert pa.check_error(ws) == 0
+    assert np.array_equal(kept.cpu().numpy(), want[0]) and np.array_equal(new.cpu().numpy(), want[1])
+    assert np.array_equal(Wt.cpu().numpy(), want[4], equal_nan=True)
+    assert np.array_equal(tile_rows(c.k, "bf16", 64), want[2]) and np.array_equal(tile_rows(c.v, "bf16", 64), want[3])
 
 
 def test_evict_of_empty_sequences_and_to_nothing():
