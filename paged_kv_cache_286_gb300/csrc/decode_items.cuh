@@ -12,7 +12,8 @@ struct DecodeParams {
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* qsl;
-  int32_t* item_start;
+  int32_t* item_start;     // [S+1] item prefix sums over the sequences in item_order
+  int32_t* item_order;     // [S] the sequences, those of the longest items first, or NULL: as they are
   int32_t* pf_item_start;  // [S+1] prefill item prefix sums over the runs in claim order
   int32_t* pf_order;       // [S] the runs with prefill items, longest item first
   int32_t* merge_start;    // [S+1] prefix sums of the rows the merge combines
@@ -99,12 +100,12 @@ __device__ __forceinline__ ItemInfo claim_item(const DecodeParams& p, int total_
       const int mid = (lo + hi) >> 1;
       if (p.item_start[mid] <= item) lo = mid; else hi = mid;
     }
-    const int s = lo;
+    const int s = p.item_order ? p.item_order[lo] : lo;
     const int t0 = p.qsl[s];
     const int n = p.qsl[s + 1] - t0;
     const int L = p.context_lens[s];
     const int tpt = R / (p.group * HPI);
-    const int istart = p.item_start[s];
+    const int istart = p.item_start[lo];
     const int qtiles = ceil_div(n, tpt);
     const int nblk = ceil_div(L, kBlockSize);
     const int nparts = ceil_div(nblk, p.pblk);

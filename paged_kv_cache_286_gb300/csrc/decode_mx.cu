@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT, HPI>::kCtas)
         auto p_half = [&](int rt, int b, int i) {
           return movmatrix_t(pack_f16x2(pr[rt][2 * i] * fv[i][b], pr[rt][2 * i + 1] * fv[i][b]));
         };
-        uint32_t pt[NB][2];  // (several heads: used for each)
+        [[maybe_unused]] uint32_t pt[NB][2];  // (several heads: used for each)
         if constexpr (HPI > 1) {
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
