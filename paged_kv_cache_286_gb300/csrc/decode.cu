@@ -1135,10 +1135,9 @@ cudaError_t launch_attention(const AttnArgs& a, const WsLayout& ws, const PoolMa
   p.rows_per_tile = mx ? (staged ? 8 : 8 * mx_row_tiles(a.max_query_len, p.group)) : rt2 ? 16 : 8;
   // Items of two heads are few and long, and sequences in their own order then leave CTAs idle at the
   // end: 256 decodes of 1,000 tokens on average, 32 q heads on 8, 104 -> 99 us over MXFP4, 130 -> 127
-  // over E4M3.  Elsewhere the order gains nothing and costs the plan about 1 us.  (So it does where
-  // all items run at once.)
-  if (hpi == 2 && a.num_seqs > 1 &&
-      static_cast<int64_t>(a.num_seqs) * (a.num_kv_heads / hpi) * ws.pmax > 4 * int64_t(p.sms))
+  // over E4M3.  Elsewhere the order gains nothing and costs the plan about 1 us; so it does for few
+  // sequences, whose items all run at once or are whole partitions (16 of 32,768: 112 -> 114).
+  if (hpi == 2 && static_cast<int64_t>(a.num_seqs) * (a.num_kv_heads / hpi) > 2 * int64_t(p.sms))
     p.item_order = reinterpret_cast<int32_t*>(wsb + ws.item_order);
   p.lse = a.lse;
   p.scores = a.scores;

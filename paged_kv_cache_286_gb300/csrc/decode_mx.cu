@@ -24,10 +24,10 @@
 //    so far (moved only when a scale exceeds it by more than 2^7, when O's columns of the block
 //    are rescaled).  Smaller scales lose nothing but what is below f16's subnormals, 2^-24 of
 //    the block's largest scale.
-//  * Measured: 256 sequences of 1,000 keys on average, 32 q heads on 8 of 128 dims: 94 us for 375 MB
-//    of tiles (4.0 TB/s); 16 x 32,768 keys 105 us (5.4 TB/s).  Bound by issue: a (block, kv head)
-//    takes some 300 warp instructions (conversions, scales, softmax, copies), near three quarters
-//    of the SM's issue slots, while DRAM waits.
+//  * Measured: 256 sequences of 1,000 keys on average, 32 q heads on 8 of 128 dims: 93 us for 388 MB
+//    of tiles (4.2 TB/s); 16 x 32,768 keys 106 us (5.4 TB/s).  A (block, kv head) takes some 270
+//    warp instructions (conversions, scales, softmax, copies): half of the SM's issue slots and of
+//    its ALU's, with dependent chains in three warps per scheduler for the rest, while DRAM waits.
 //  * The softmax base of a row moves only when a score exceeds it by more than 2^8, so that the
 //    usual block needs one warp vote and no maximum across lanes.
 #include <math_constants.h>
@@ -699,7 +699,7 @@ int mx_row_tiles(int32_t max_query_len, int32_t group) {
 
 // Two kv heads per item where their rows fill an 8-row tile that one head's would leave half
 // empty: what a block costs beside its codes (softmax, scales, the copies' and items' bookkeeping)
-// is then paid once for two.  256 decodes of 1,000 tokens on average, 32 q heads on 8: 121 -> 105
+// is then paid once for two.  256 decodes of 1,000 tokens on average, 32 q heads on 8: 121 -> 104
 // us.
 //
 // With the bound on the contexts, few items may come to a CTA, and their last round then leaves

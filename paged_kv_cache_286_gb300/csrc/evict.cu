@@ -9,7 +9,7 @@
 //    same order, which stay in shared memory; three histogram passes of 11, 11 and 10 bits find
 //    the (k - r)-th largest and how many of its equals are kept; a last pass, in order, compacts
 //    the kept positions, whose weights are then moved.
-//    Instructions bound it, some 100 per 32 keys, then the latency of its eleven barriers: 16 x 8
+//    Instructions bound it, some 80 per 32 keys, then the latency of its eleven barriers: 16 x 8
 //    rows of 32,768 weights 24 us, 64 x 32 rows of 2,300 on average 37 us.
 //  * move_kernel: one CTA per (sequence, kv head, K or V, column slice).  A kept key never moves
 //    up, so rows can move in place if a batch of them is read before it is written and batches go

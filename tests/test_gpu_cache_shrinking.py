@@ -325,6 +325,33 @@ def test_mxfp4_small_groups(hq, hkv, d, qlens, spread):
     check_weights(c, before, W.cpu().numpy(), list(range(len(lens))), 1.0)
 
 
+@pytest.mark.parametrize("kind", ["mxfp4", "e4m3"])
+def test_many_sequences_of_two_heads_per_item(kind):
+    """More sequences than the plan orders at a time, in its order of length: some without query
+    tokens, some of one key, and one that breaks the bound on contexts and is left out."""
+    import paged_kv_cache_286_gb300 as pa
+    rng = np.random.default_rng(41)
+    lens = rng.integers(1, 200, 1100)
+    lens[::7] = 1
+    lens[[5, 1030]] = [1500, 1400]
+    qlens = (rng.random(1100) < 0.9).astype(np.int32)
+    qlens[[5, 9, 1030]] = 1
+    c = Case(lens, qlens, 8, 2, 128, kind, seed=42)
+    t, ctx, qsl = c.dev()
+    ws = c.workspace(pa)
+    ws[256:] = 0xFF
+    out = pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, **c.hints())
+    assert pa.check_error(ws) == 0
+    check_mx(c, out)
+    ctx[9] = 1501
+    row = int(c.qsl[9])
+    again = torch.full_like(out, 7.0)
+    pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, out=again, **c.hints())
+    assert pa.check_error(ws, raise_on_error=False) == 0x4
+    out[row] = 7.0
+    assert torch.equal(again, out)
+
+
 @pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (16, 8, 64)])
 def test_mxfp4_partitions_cut_to_even_rounds(hq, hkv, d):
     """Contexts of up to 3,000 keys under a bound for which the partitions are longer than 128 blocks."""
