@@ -60,7 +60,8 @@ struct MxCfg {
 };
 
 // kScores: the scores of runs of up to kDecodeMaxRows rows are also written out, for the key
-// weights (key_weights.cu).
+// weights (key_weights.cu): 256 sequences of 2,000 keys, 32 q heads on 8, 130 -> 158 us with the
+// weights made of them.
 // HPI kv heads per item: row r of a token is q head h * G + r, and the rows of head h + i take
 // their scores from, and add P V into O from, head i's tiles alone.  A lane's two rows are of one
 // head (an even group).
@@ -260,6 +261,15 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT, HPI>::kCtas)
 #pragma unroll
     for (int b = 0; b < NB; ++b) vinv[b] = __uint_as_float(254u << 23);
 
+    // scores of this lane's first row and key: rows are (token, q head) of the head's run, so the
+    // next row, and with one head per item row 8, follow at their stride
+    [[maybe_unused]] float* my_scores = nullptr;
+    if constexpr (kScores) {
+      const int per_tok = p.group * HPI, row = 2 * qc;
+      my_scores = p.scores + ((static_cast<int64_t>(I.s) * p.num_kv_heads + I.h + my_head) * p.score_rows +
+                              (I.qt * (R / per_tok) + row / per_tok) * p.group +
+                              (HPI == 1 ? row % per_tok : row % p.group)) * p.score_stride + my_key;
+    }
     bool fresh = true;  // no block of the item is in O yet
     // One block: `diag` if some row of the item does not see some of its keys.
     auto tile_step = [&](int k, int st, auto diag_tag) {
@@ -369,15 +379,10 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT, HPI>::kCtas)
           for (int rt = 0; rt < RT; ++rt) {
             if (I.run * p.group > p.score_rows) break;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = 8 * rt + 2 * qc + (i & 1);  // (token, head of the item, q head)
-              const int tok = row / (p.group * HPI);
-              if (row < I.rows)
-                p.scores[((static_cast<int64_t>(I.s) * p.num_kv_heads + I.h + my_head) * p.score_rows +
-                          (I.qt * (R / (p.group * HPI)) + tok) * p.group + row % p.group) *
-                             p.score_stride +
-                         key0 + my_key + 8 * (i >> 1)] = s[rt][i] * row_scale[rt][i & 1];
-            }
+            for (int i = 0; i < 4; ++i)
+              if (8 * rt + 2 * qc + (i & 1) < I.rows)
+                my_scores[(8 * rt + (i & 1)) * p.score_stride + key0 + 8 * (i >> 1)] =
+                    s[rt][i] * row_scale[rt][i & 1];
           }
         }
 

@@ -15,8 +15,8 @@
 //    and read four or eight times the bytes.
 //  * A score costs the epilogue an FMA, a 2^x and an add; the 2^x bound it from below (32 a cycle
 //    and SM: 0.5 us a tile of 256 x 128), the MMAs take about as long.  Two runs of 2,048 tokens
-//    x 32 heads after 6,144 (8 kv heads of 128): 338 us for bf16 keys, 712 TFLOP/s, 349 us for E4M3
-//    and 350 us for MXFP4, where the mma.sync kernel took 1,280; one run of 512 x 32 in 2,560 keys
+//    x 32 heads after 6,144 (8 kv heads of 128): 338 us for bf16 keys, 712 TFLOP/s, 341 us for E4M3
+//    and 344 us for MXFP4, where the mma.sync kernel took 1,280; one run of 512 x 32 in 2,560 keys
 //    beside one of 512 x 32 in 512 31 us.
 //  * Every wait is bounded; when one runs out the CTA records PA_DEVERR_TIMEOUT, stops, lets its
 //    copies and MMAs finish (bounded again) and frees its tensor memory.
@@ -242,17 +242,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // the item's keys, converted by these warps: 16-byte pieces (8 dims) of the K tiles' layout
         constexpr int kEach = kTcKeys * (D / 8) / (32 * kTcEpilogue);
         const uint32_t ks = kc % kTcKStages;
+        // (without branches, so that all the table's entries, then all the keys load at once; what
+        // is not there reads the pool's first block and becomes zeros)
+        int phys[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const int kk = ((i * kTcEpilogue + e) * 32 + lane) / (D / 8);
+          phys[i] = __ldg(a.block_tables + static_cast<int64_t>(I.s) * a.max_blocks_per_seq +
+                          min(I.base + kk, I.L - 1) / kBlockSize);
+        }
         uint32_t w[kEach][4];
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
           const int piece = (i * kTcEpilogue + e) * 32 + lane, kk = piece / (D / 8), c = piece % (D / 8);
-          w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
-          if (I.base + kk >= I.L) continue;
-          const int phys = __ldg(a.block_tables + static_cast<int64_t>(I.s) * a.max_blocks_per_seq +
-                                 (I.base + kk) / kBlockSize);
-          if (phys < 0 || phys >= a.num_blocks) continue;  // (flagged by the attention)
-          load_dims<kPool, D>(a.k_cache, static_cast<int64_t>(phys) * a.num_kv_heads + I.h,
+          const bool there = I.base + kk < I.L && phys[i] >= 0 && phys[i] < a.num_blocks;
+          load_dims<kPool, D>(a.k_cache, (there ? int64_t{phys[i]} : 0) * a.num_kv_heads + I.h,
                               kk % kBlockSize, c >> 2, c & 3, w[i]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) w[i][x] = there ? w[i][x] : 0u;  // (bad blocks are flagged by the attention)
         }
         if (!(ok = wait(&ctl.k_empty[ks], ((kc / kTcKStages) & 1u) ^ 1u))) break;
         const uint32_t base = smem_u32(smem + L::kK + ks * 2 * L::kTile);
