@@ -116,8 +116,9 @@ typedef struct {
  * nearest.  MXFP4 pools receive, per block of 32 dims, the scale 2^e with e = floor(log2(amax)) -
  * 2 (at least -127; amax the block's largest magnitude) and, per element, x / 2^e rounded to the
  * nearest E2M1 value (ties to the even code, saturating at +-6); a block with a NaN receives the
- * NaN scale and zero codes.  num_tokens == 0 is a no-op.  A slot written twice in one call ends up holding one
- * of the writes. */
+ * NaN scale and zero codes.  num_tokens == 0 is a no-op.  A slot written twice in one call ends up
+ * holding one of the writes; in an MXFP4 pool its codes and scales may be of different ones, so
+ * there a call's slots must differ. */
 pa_status pa_cache_append(const void* k, const void* v, const int64_t* slot_mapping,
                           int32_t num_tokens, void* k_cache, void* v_cache,
                           const pa_cache_desc* cache, void* workspace, cudaStream_t stream);

@@ -68,9 +68,8 @@ __device__ __forceinline__ int kw_chunks(const KeyWeightsArgs& a, int s, uint32_
 // L2's) and by launch.
 constexpr int kFinThreads = 256;
 constexpr int kFinShare = 4096;  // keys of a share at least (of the longest sequence)
-__global__ void __launch_bounds__(kFinThreads) kw_finish_kernel(const KeyWeightsArgs a) {
+__device__ __forceinline__ void finish_share(const KeyWeightsArgs& a) {
   __shared__ float s_lse[kDecodeMaxRows];
-  grid_dependency_wait();
   const int s = blockIdx.x, h = blockIdx.y;
   uint32_t bits = 0;
   const bool ok = kw_accumulates(a, s, &bits);
@@ -131,6 +130,19 @@ __global__ void __launch_bounds__(kFinThreads) kw_finish_kernel(const KeyWeights
     for (int i = 0; i < 4; ++i)
       if (key + i < L) W[key + i] = fmaf(a.decay, w[i], sum[i]);
   }
+}
+
+// kBeside: launched after the tensor-core kernel, which has other sequences and lets it start once the
+// attention is complete, it waits for that kernel only at its end.  In 40 registers a CTA fits in
+// what one of that kernel's leaves of an SM (48 decodes beside two runs of 512: 138.8 -> 133.9 us,
+// with 60 registers 137.6).  Alone, five CTAs to an SM: 256 sequences of 1,000 keys on average,
+// the whole step 159 us; with six 161, with three 163.
+template <bool kBeside>
+__global__ void __launch_bounds__(kFinThreads, kBeside ? 6 : 5)
+    kw_finish_kernel(const KeyWeightsArgs a) {
+  if (!kBeside) grid_dependency_wait();
+  finish_share(a);
+  if (kBeside) grid_dependency_wait();
 }
 
 // One CTA: exclusive prefix sums of the sequences' chunks.
@@ -382,19 +394,24 @@ cudaError_t run_key_weights(const KeyWeightsArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_key_weights(KeyWeightsArgs a, const PoolMaps* maps, cudaStream_t stream) {
   a.chunk_keys = maps ? kKeyWeightsTcKeys : kKwKeys;
-  cudaError_t e = cudaSuccess;
-  if (a.scores) {
+  const bool beside = a.k_pass && maps;  // of the tensor-core kernel, on the SMs that it leaves idle
+  auto finish = [&] {
     const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
     const int64_t shares = std::min<int64_t>((a.max_context_len + int64_t(kFinShare) - 1) / kFinShare, 65535);
     if (pairs > INT32_MAX || a.num_kv_heads > 65535) return cudaErrorInvalidValue;
-    e = launch_dependent(kw_finish_kernel, dim3(a.num_seqs, a.num_kv_heads, unsigned(shares)),
-                         dim3(kFinThreads), 0, stream, a);
-    if (e != cudaSuccess) return e;
-  }
+    return launch_dependent(beside ? kw_finish_kernel<true> : kw_finish_kernel<false>,
+                            dim3(a.num_seqs, a.num_kv_heads, unsigned(shares)), dim3(kFinThreads),
+                            0, stream, a);
+  };
+  cudaError_t e = cudaSuccess;
+  if (a.scores && !beside && (e = finish()) != cudaSuccess) return e;
   if (!a.k_pass) return cudaSuccess;
   e = launch_dependent(kw_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
   if (e != cudaSuccess) return e;
-  if (maps) return launch_key_weights_tc(a, *maps, stream);
+  if (maps) {
+    e = launch_key_weights_tc(a, *maps, stream);
+    return e == cudaSuccess && a.scores ? finish() : e;
+  }
   if (a.cache_dtype == PA_FP8_E4M3) return run_key_weights<Pool::kE4m3, 128>(a, stream);
   if (a.cache_dtype == PA_MXFP4)
     return a.head_dim == 128 ? run_key_weights<Pool::kMx, 128>(a, stream)

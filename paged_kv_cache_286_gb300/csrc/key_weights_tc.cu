@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
   grid_dependency_wait();
+  grid_launch_dependents();  // the finishing kernel, which has other sequences, may start beside
   const int G = a.num_q_heads / a.num_kv_heads, tpt = 128 / G;
   const int64_t total = static_cast<int64_t>(a.chunk_start[a.num_seqs]) * a.num_kv_heads;
 
