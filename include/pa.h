@@ -40,8 +40,9 @@
  *                bf16, or OCP E4M3 bytes holding x / k_scale (resp. v_scale) with fp32 per-tensor
  *                scales.  One (block, kv head) tile of block_size x head_dim is contiguous.
  *                PA_MXFP4 pools (microscaled 4-bit floating point): 32 neighbouring dims of a row
- *                share a scale byte e (E8M0: 2^(e - 127), 255 = NaN), and a dim is a 4-bit E2M1
- *                code c (0 .5 1 1.5 2 3 4 6, bit 3 the sign): value = code * 2^(e - 127).  One
+ *                share a scale byte e (E8M0: 2^(e - 127), 255 = NaN, with codes of zero), and a dim
+ *                is a 4-bit E2M1 code c (0 .5 1 1.5 2 3 4 6, bit 3 the sign): value = code *
+ *                2^(e - 127), subnormal results included.  One
  *                (block, kv head) tile is 17 * head_dim / 2 contiguous bytes: 16 rows of
  *                head_dim / 2 bytes of codes, then 16 rows of head_dim / 32 scale bytes.  With
  *                nb = head_dim / 32, 16-bit word g * nb + b of a row (little endian) holds dims

@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(256) cache_read_mx_kernel(
     const int off = static_cast<int>(slot % kBlockSize);
     const int64_t tile = static_cast<int64_t>(blk * heads.d + h) * (NB * 32 * 17 / 2);
     const int64_t scale_at = tile + kBlockSize * 16 * NB + off * NB + ((lane >> 2) & (NB - 1));
-    const float ks = e8m0_to_f32(__ldg(k_cache + scale_at), 0);
-    const float vs = e8m0_to_f32(__ldg(v_cache + scale_at), 0);
+    const float ks = e8m0_to_f32(__ldg(k_cache + scale_at));
+    const float vs = e8m0_to_f32(__ldg(v_cache + scale_at));
     bool upper;
     const int at = mx_piece<NB>(lane, &upper);
     uint2 w = __ldg(reinterpret_cast<const uint2*>((upper ? v_cache : k_cache) + tile +

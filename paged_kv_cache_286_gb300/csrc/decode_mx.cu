@@ -43,6 +43,13 @@
 
 namespace pa {
 
+// max of three, NaN if one of them is
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <int D, int RT, int HPI>
 struct MxCfg {
   static constexpr int kStages = HPI == 1 && RT == 1 ? 4 : 3;
@@ -307,6 +314,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT, HPI>::kCtas)
           float sh[RT][4];
 #pragma unroll
           for (int bp = 0; bp < NB / 2; ++bp) {  // scale blocks 2 bp and 2 bp + 1
+            const uint32_t sc2_lo = e8m0x2_to_bf16x2(ks[0], bp), sc2_hi = e8m0x2_to_bf16x2(ks[1], bp);
             // words of dims 4 g .. of both blocks: g = 2 qc in word bp, 2 qc + 1 in NB / 2 + bp
             uint32_t lo[2][4], up[2][4];
 #pragma unroll
@@ -317,7 +325,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT, HPI>::kCtas)
 #pragma unroll
             for (int bb = 0; bb < 2; ++bb) {
               const int b = 2 * bp + bb;
-              const float sc_lo = e8m0_to_f32(ks[0], b), sc_hi = e8m0_to_f32(ks[1], b);
+              const float sc_lo = bb ? bf16hi_to_f32(sc2_lo) : bf16lo_to_f32(sc2_lo);
+              const float sc_hi = bb ? bf16hi_to_f32(sc2_hi) : bf16lo_to_f32(sc2_hi);
 #pragma unroll
               for (int rt = 0; rt < RT; ++rt) {
                 if (RT > 1 && 8 * rt >= I.rows) break;
@@ -411,13 +420,17 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT, HPI>::kCtas)
 #pragma unroll 1
         for (bool again = true;; again = false) {
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            fv[0][b] = e8m0_to_f32(vs[0], b) * vinv[b];
-            fv[1][b] = e8m0_to_f32(vs[1], b) * vinv[b];
-          }
-          float fmax = fmaxf(fv[0][0], fv[1][0]), pmax = 0.f;
+          for (int b = 0; b < NB; b += 2) {
 #pragma unroll
-          for (int b = 1; b < NB; ++b) fmax = fmax3(fmax, fv[0][b], fv[1][b]);
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t f = e8m0x2_to_bf16x2(vs[i], b / 2);
+              fv[i][b] = bf16lo_to_f32(f) * vinv[b];
+              fv[i][b + 1] = bf16hi_to_f32(f) * vinv[b + 1];
+            }
+          }
+          float fmax = 0.f, pmax = 0.f;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) fmax = fmax3_nan(fmax, fv[0][b], fv[1][b]);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             if (RT > 1 && 8 * rt >= I.rows) break;
@@ -429,7 +442,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT, HPI>::kCtas)
             }
             pmax = fmax3(fmax3(pr[rt][0], pr[rt][1], pr[rt][2]), pr[rt][3], pmax);
           }
-          if (!__any_sync(0xffffffffu, again && (fmax > 128.f || pmax > 256.f))) break;
+          if (!__any_sync(0xffffffffu, again && (!(fmax <= 128.f) || pmax > 256.f))) break;
           // (O is rescaled only if something is in it)
           if (__any_sync(0xffffffffu, pmax > 256.f)) {
 #pragma unroll
@@ -460,7 +473,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT, HPI>::kCtas)
               }
             }
           }
-          if (__any_sync(0xffffffffu, fmax > 128.f)) {
+          if (__any_sync(0xffffffffu, !(fmax <= 128.f))) {
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               const int e0 = (vs[0] >> (8 * b)) & 255, e1 = (vs[1] >> (8 * b)) & 255;
@@ -618,7 +631,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT, HPI>::kCtas)
 #pragma unroll
         for (int n = 0; n < 2 * NB; ++n) {
           // 2^(R_b - 127)
-          const float up = __uint_as_float((254u << 23) - __float_as_uint(vinv[n >> 1]));
+          const float up = e8m0_to_f32(254u - (__float_as_uint(vinv[n >> 1]) >> 23));
           *reinterpret_cast<float2*>(so + row * D + 32 * (n >> 1) + 4 * quad + 2 * (n & 1)) =
               make_float2(oacc[rt][n][j] * up, oacc[rt][n][2 + j] * up);
         }

@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(2 * D) mx_stage_kernel(
       const uint16_t* src = reinterpret_cast<const uint16_t*>(t + row * Mx<D>::kRowBytes);
       const uint32_t codes = __ldg(src + g * NB + b) |
                              (static_cast<uint32_t>(__ldg(src + (g + 1) * NB + b)) << 16);
-      const float sc = e8m0_to_f32(__ldg(t + Mx<D>::kCodeBytes + row * NB + b), 0);
+      const float sc = e8m0_to_f32(__ldg(t + Mx<D>::kCodeBytes + row * NB + b));
       uint32_t f[4], w[4];
       e2m1x8_to_f16x2x4(codes, f);
 #pragma unroll

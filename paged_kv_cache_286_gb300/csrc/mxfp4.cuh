@@ -1,6 +1,6 @@
 // MXFP4 pool tiles: E2M1 codes (sign, two exponent bits, one mantissa bit: 0 .5 1 1.5 2 3 4 6) in
 // blocks of 32 dims of a row that share one E8M0 scale byte e, which stands for 2^(e - 127)
-// (255: NaN).
+// (255: NaN; the codes of such a block are zeros).
 //
 // One (block, kv head) tile is 16 rows of D / 2 bytes of codes, then 16 rows of D / 32 scale
 // bytes: 17 D / 2 bytes, a multiple of 16.  Within a row, 16-bit word g * (D / 32) + b holds
@@ -47,11 +47,17 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&x)[8]) {
   return out;
 }
 
-// Scale byte `i` of a word as fp32.  Byte 0 gives 0 instead of 2^-127 (what it scales is below
-// fp32's normal range), and byte 255 gives infinity: the codes of a NaN block are zeros, so their
-// product with it is NaN.
-__device__ __forceinline__ float e8m0_to_f32(uint32_t word, int i) {
-  return __uint_as_float(i == 3 ? (word >> 1) & 0x7f800000u : (word << (23 - 8 * i)) & 0x7f800000u);
+// Two neighbouring scale bytes (a half of the word) as a bf16 pair, exactly: byte 0 is the subnormal
+// 2^-127 (codes times it are up to 1.5 * 2^-125), byte 255 NaN.
+__device__ __forceinline__ uint32_t e8m0x2_to_bf16x2(uint32_t word, int half) {
+  uint32_t out;
+  asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(out) : "h"(static_cast<uint16_t>(word >> (16 * half))));
+  return out;
+}
+
+// One scale byte as fp32.
+__device__ __forceinline__ float e8m0_to_f32(uint32_t byte) {
+  return bf16lo_to_f32(e8m0x2_to_bf16x2(byte, 0));
 }
 
 // Transposes the 8 x 8 matrix of 16-bit elements that the warp holds two to a lane.

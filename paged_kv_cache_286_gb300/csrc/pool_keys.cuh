@@ -29,7 +29,7 @@ __device__ __forceinline__ void load_dims(const uint8_t* __restrict__ k_cache, i
     const uint16_t* src = reinterpret_cast<const uint16_t*>(t + off * Mx<D>::kRowBytes);
     const uint32_t codes = __ldg(src + 2 * qc * NC + c) |
                            (static_cast<uint32_t>(__ldg(src + (2 * qc + 1) * NC + c)) << 16);
-    const float sc = e8m0_to_f32(__ldg(t + Mx<D>::kCodeBytes + off * NC + c), 0);
+    const float sc = e8m0_to_f32(__ldg(t + Mx<D>::kCodeBytes + off * NC + c));
     uint32_t f[4];
     e2m1x8_to_f16x2x4(codes, f);
 #pragma unroll

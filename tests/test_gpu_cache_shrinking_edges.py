@@ -1,0 +1,106 @@
+"""Edges of the operators that shrink the cache, on the GPU, against the definitions in 64 bits: the
+smallest scales of MXFP4 pools.
+
+Tolerances are those of test_gpu_cache_shrinking.py (a score off by less than 2e-4 in the log2 domain,
+so a weight or a log-sum-exp's power by 4e-4; MXFP4 attention rounds a probability to f16, 2^-12);
+codes, bytes, positions and moves are exact."""
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_cache_shrinking import BS, Case, bits_f64, check_weights, mx_inputs
+
+pytestmark = pytest.mark.gpu
+
+from oracle import mxfp4  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from paged_kv_cache_286_gb300 import build
+    build.build()
+
+
+# ---------------------------------------------------------------------------------------------
+# the smallest scales: byte 0 is 2^-127, whose codes reach 1.5 * 2^-125
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("d,hkv,T", [(128, 8, 301), (64, 3, 97), (128, 1, 33), (64, 1, 1024)])
+def test_mxfp4_append_and_read_of_every_scale(d, hkv, T):
+    import paged_kv_cache_286_gb300 as pa
+    k, v = mx_inputs(d, T, hkv, 1), mx_inputs(d, T, hkv, 2)
+    # whole blocks of the two smallest scales: every multiple of 2^-128, and of 2^-129, up to 31
+    tiny = np.arange(T * hkv * d).reshape(T, hkv, d) % 32 * 2.0 ** -128
+    k[T - 9:] = torch.from_numpy(tiny[T - 9:]).bfloat16()
+    v[T - 9:] = -k[T - 9:] / 2
+    nb = T // BS + 3
+    slots = np.random.default_rng(3).permutation(nb * BS)[:T].astype(np.int64)
+    slots[4] = -1
+    kc, vc = pa.new_mxfp4_cache(nb, hkv, d), pa.new_mxfp4_cache(nb, hkv, d)
+    ws = pa.new_workspace(256)
+    ts = torch.from_numpy(slots).cuda()
+    pa.cache_append(k.cuda(), v.cuda(), ts, kc, vc, ws)
+    outs = {t: pa.cache_read(ts, kc, vc, ws, out_dtype=t) for t in (torch.bfloat16, torch.float32)}
+    assert pa.check_error(ws) == 0
+    for i, x in enumerate((k, v)):
+        codes, byte = mxfp4.encode(bits_f64(x))
+        want = mxfp4.decode(codes, byte)
+        assert want[T - 9:].any() and (byte[T - 9:] == 1 - i).all()
+        want[4] = 0.0
+        for t in outs:
+            assert outs[t][i].dtype == t
+            assert np.array_equal(outs[t][i].float().cpu().numpy(), want.astype(np.float32), equal_nan=True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_mxfp4_read_of_any_bytes(d):
+    """Every scale byte beside every code; 6 * 2^127 is past fp32's and bf16's range."""
+    import paged_kv_cache_286_gb300 as pa
+    pool = np.random.default_rng(d).integers(0, 256, (2, 20, 3, 17 * d // 2), dtype=np.uint8)
+    want = mxfp4.decode(*mxfp4.unpack_tiles(pool[0])), mxfp4.decode(*mxfp4.unpack_tiles(pool[1]))
+    slots = torch.arange(20 * BS, device="cuda")
+    ws = pa.new_workspace(256)
+    for t in (torch.bfloat16, torch.float32):
+        got = pa.cache_read(slots, *(torch.from_numpy(p).cuda() for p in pool), ws, out_dtype=t)
+        assert pa.check_error(ws) == 0
+        for g, w in zip(got, want):
+            with np.errstate(over="ignore"):
+                w = w.transpose(0, 2, 1, 3).reshape(-1, 3, d).astype(np.float32)
+            assert np.array_equal(g.float().cpu().numpy(), w, equal_nan=True)
+
+
+def smallest(c, which):
+    """The case with its keys or values in blocks of scale bytes 0 and 1."""
+    vals = c.kv if which == "k" else c.vv
+    codes, byte = mxfp4.encode(np.where(np.isfinite(vals), vals, 0.0) * 2.0 ** -126)
+    assert byte.max() <= 1 and (byte == 0).mean() > 0.5
+    pool, vals = torch.from_numpy(mxfp4.pack_tiles(codes, byte)).cuda(), mxfp4.decode(codes, byte)
+    if which == "k":
+        c.k, c.kv = pool, vals
+        c.q = (c.q.float() * 2.0 ** 112).bfloat16()                  # scores of the usual size
+        c.scale *= 2.0 ** 14
+    else:
+        c.v, c.vv = pool, vals
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("d,hq,hkv", [(128, 8, 2), (64, 4, 4), (128, 2, 2), (64, 16, 1)])
+@pytest.mark.parametrize("qlens", [(1, 1, 1, 1), (1, 3, 2, 1), (40, 1, 60, 2)])
+def test_mxfp4_attention_over_the_smallest_scales(which, d, hq, hkv, qlens):
+    """Decode tokens, short runs and staged chunks, their weights too."""
+    import paged_kv_cache_286_gb300 as pa
+    c = Case([700, 33, 90, 16], qlens, hq, hkv, d, "mxfp4", seed=d + hq)
+    smallest(c, which)
+    t, ctx, qsl = c.dev()
+    before = np.zeros((4, hkv, 700), np.float32)
+    W = torch.from_numpy(before).cuda()
+    ws, ref = c.workspace(pa, True), c.reference()[0]
+    ws[256:] = 0xFF
+    out = pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, ctx, qsl, W, ws, **c.hints())
+    assert pa.check_error(ws) == 0
+    got = bits_f64(out)
+    top = np.abs(c.vv).max()
+    # 2^-149: outputs of the smallest values are subnormal
+    assert np.abs(got - ref).max() <= (2.0 ** -12 + 4e-4) * top + 8 * 2.0 ** -149
+    assert np.abs(ref).max() > 0.1 * top
+    check_weights(c, before, W.cpu().numpy(), list(range(4)), 1.0)
