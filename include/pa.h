@@ -237,8 +237,9 @@ size_t pa_evict_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t m
  *   dst_tables    the same shape: where they go, or NULL for block_tables (in place).  Entry i may
  *                 be block_tables' entry i, or a block that no sequence of the call reads; no
  *                 block may be a destination of two sequences, and none that another sequence
- *                 reads may be a destination (pa_bm_evict gives such tables); otherwise the
- *                 blocks' contents are undefined.
+ *                 reads may be a destination (one pa_bm_evict_batch call gives such tables for its
+ *                 sequences; several pa_bm_evict calls do not); otherwise the blocks' contents are
+ *                 undefined.  (A key that keeps its place is neither read nor written.)
  *   keep_lens     [num_seqs] int32 (device), >= 0.
  *   max_context_len, max_keep_len   host upper bounds of context_lens and of k.
  *   key_weights, weight_rows, num_weight_rows, max_keys   as in pa_attention_key_weights.  The

@@ -78,16 +78,27 @@ int32_t pa_bm_fork(pa_block_manager* bm, int64_t parent, int64_t child);
  * free list, or to the evictable cache if it carries a hash).  Returns 0 or PA_BM_BAD_ARG. */
 int32_t pa_bm_free(pa_block_manager* bm, int64_t seq);
 
-/* Reduce seq to its first `keep` token positions before pa_evict_keys fills them with the kept
- * keys.  The sequence's new table has ceil(keep / block_size) blocks: blocks that other
- * sequences share are replaced by fresh ones, blocks that it holds alone stay (and leave the
- * prefix cache, as their contents change); its other blocks are released.  The new table goes
- * to table_out, padded with -1 to cap entries: with the table from before the call as
- * block_tables it is pa_evict_keys' dst_tables.  Released blocks may be handed out by the next
- * call, so pa_evict_keys must be launched before, on the same stream as, the kernels that write
- * them.  Tokens appended later carry no hash.
- * Returns the number of blocks, PA_BM_NO_SPACE, or PA_BM_BAD_ARG (unknown sequence, keep < 0 or
- * above its tokens, cap too small). */
+/* Reduce n sequences to their first keeps[i] token positions before one pa_evict_keys call fills
+ * these with the kept keys.  A sequence's new table has ceil(keeps[i] / block_size) blocks: blocks
+ * that another sequence shares before the call are replaced by fresh ones, blocks that it holds
+ * alone stay (and leave the prefix cache, as their contents change); its other blocks are released,
+ * after every fresh block has been taken.  So no block of a new table that is written is one that
+ * another sequence of the call reads or writes.  A sequence with keeps[i] equal to its tokens keeps
+ * its table, shared blocks included: none of its keys moves.
+ * The new tables go to tables_out [n][width], padded with -1: with the tables from before the call
+ * as block_tables they are pa_evict_keys' dst_tables.  Released blocks may be handed out by the
+ * next call, so pa_evict_keys must be launched before, on the same stream as, whatever writes
+ * those: another pa_evict_keys for tables of a later call among them.  Tokens appended later carry
+ * no hash.
+ * Returns 0, PA_BM_NO_SPACE, or PA_BM_BAD_ARG (unknown sequence or one named twice, keeps[i] < 0 or
+ * above its tokens, width too small). */
+int32_t pa_bm_evict_batch(pa_block_manager* bm, const int64_t* seqs, const int64_t* keeps, int32_t n,
+                          int32_t* tables_out, int32_t width);
+
+/* pa_bm_evict_batch of one sequence, its table in table_out[0..cap).  Tables of several such calls
+ * may name each other's blocks: each needs a pa_evict_keys of its own, launched in the order of the
+ * calls on one stream.
+ * Returns the number of blocks, PA_BM_NO_SPACE, or PA_BM_BAD_ARG. */
 int32_t pa_bm_evict(pa_block_manager* bm, int64_t seq, int64_t keep, int32_t* table_out,
                     int32_t cap);
 

@@ -29,7 +29,8 @@ EXPORTED = ["pa_cache_append", "pa_attention_workspace_size", "pa_attention", "p
             "pa_test_skip_one_copy", "pa_selftest_wait_timeout"]
 EXPORTED_BM = ["pa_bm_create", "pa_bm_destroy", "pa_bm_num_free", "pa_bm_append",
                "pa_bm_append_tokens", "pa_bm_fork", "pa_bm_free", "pa_bm_block_table",
-               "pa_bm_num_tokens", "pa_bm_refcount", "pa_bm_cached_prefix", "pa_bm_evict"]
+               "pa_bm_num_tokens", "pa_bm_refcount", "pa_bm_cached_prefix", "pa_bm_evict",
+               "pa_bm_evict_batch"]
 
 
 class CacheDesc(ctypes.Structure):
@@ -109,6 +110,8 @@ def load() -> ctypes.CDLL:
     L.pa_bm_block_table.restype = i32
     L.pa_bm_evict.argtypes = [vp, i64, i64, vp, i32]
     L.pa_bm_evict.restype = i32
+    L.pa_bm_evict_batch.argtypes = [vp, vp, vp, i32, vp, i32]
+    L.pa_bm_evict_batch.restype = i32
     L.pa_bm_num_tokens.argtypes = [vp, i64]
     L.pa_bm_num_tokens.restype = i64
     L.pa_bm_refcount.argtypes = [vp, i32]

@@ -90,12 +90,30 @@ class BlockManager:
 
     def evict(self, seq: int, keep: int, width: Optional[int] = None) -> np.ndarray:
         """Reduce the sequence to `keep` positions; returns its new block table, padded with -1 to
-        `width` entries (evict_keys' dst_tables row beside the table from before the call)."""
+        `width` entries (evict_keys' dst_tables row beside the table from before the call).  For
+        several sequences in one evict_keys call use evict_batch: tables of separate calls may name
+        each other's blocks."""
         need = -(-max(int(keep), 0) // self.block_size)
         out = np.full(max(need, 1) if width is None else int(width), -1, dtype=np.int32)
         n = self._check(self._L.pa_bm_evict(self._h, int(seq), int(keep), out.ctypes.data,
                                             int(out.shape[0])))
         return out[:n] if width is None else out
+
+    def evict_batch(self, seqs: Sequence[int], keeps: Sequence[int],
+                    width: Optional[int] = None) -> np.ndarray:
+        """Reduce the sequences to keeps[i] positions each; returns their new block tables, int32
+        [len(seqs), width] padded with -1: dst_tables of one evict_keys call, whose block_tables are
+        the tables from before this call.  No block written for one is read for another."""
+        ids = np.ascontiguousarray(np.asarray(seqs, dtype=np.int64).reshape(-1))
+        kp = np.ascontiguousarray(np.asarray(keeps, dtype=np.int64).reshape(-1))
+        if ids.shape != kp.shape:
+            raise ValueError("seqs and keeps must have the same length")
+        if width is None:
+            width = max([-(-max(int(k), 0) // self.block_size) for k in kp] + [1])
+        out = np.full((ids.shape[0], int(width)), -1, dtype=np.int32)
+        self._check(self._L.pa_bm_evict_batch(self._h, ids.ctypes.data, kp.ctypes.data,
+                                              int(ids.shape[0]), out.ctypes.data, int(width)))
+        return out
 
     def num_tokens(self, seq: int) -> int:
         return int(self._check(self._L.pa_bm_num_tokens(self._h, int(seq))))

@@ -10,6 +10,7 @@
 #include <list>
 #include <new>
 #include <unordered_map>
+#include <unordered_set>
 #include <vector>
 
 namespace {
@@ -51,6 +52,8 @@ struct pa_block_manager {
   std::vector<std::list<int32_t>::iterator> lru_pos;
   std::vector<char> in_lru;
   std::unordered_map<int64_t, Seq> seqs;
+
+  int64_t blocks_of(int64_t tokens) const { return (tokens + bs - 1) / bs; }
 
   int32_t available() const { return static_cast<int32_t>(free_list.size() + lru.size()); }
 
@@ -251,39 +254,73 @@ int32_t pa_bm_free(pa_block_manager* bm, int64_t seq) {
   return 0;
 }
 
+int32_t pa_bm_evict_batch(pa_block_manager* bm, const int64_t* seqs, const int64_t* keeps,
+                          int32_t n, int32_t* tables_out, int32_t width) {
+  if (!bm || n < 0 || width < 0 || (n > 0 && (!seqs || !keeps)) ||
+      (n > 0 && width > 0 && !tables_out))
+    return PA_BM_BAD_ARG;
+  try {
+    std::vector<Seq*> of(n);
+    std::unordered_set<int64_t> seen;
+    int64_t shared = 0;
+    for (int32_t i = 0; i < n; ++i) {
+      auto it = bm->seqs.find(seqs[i]);
+      if (it == bm->seqs.end() || keeps[i] < 0 || keeps[i] > it->second.ntok ||
+          !seen.insert(seqs[i]).second)
+        return PA_BM_BAD_ARG;
+      of[i] = &it->second;
+      const int64_t nblk = bm->blocks_of(keeps[i]);
+      if (nblk > width) return PA_BM_BAD_ARG;
+      if (keeps[i] < of[i]->ntok)
+        for (int64_t j = 0; j < nblk; ++j) shared += bm->ref[of[i]->blocks[j]] > 1;
+    }
+    if (shared > bm->available()) return PA_BM_NO_SPACE;
+    // Fresh blocks for every block that was shared before the call come first, releases last: the
+    // blocks that one sequence leaves still hold keys that are to be moved, its own or another's.
+    std::vector<int32_t> left;
+    for (int32_t i = 0; i < n; ++i) {
+      Seq& s = *of[i];
+      if (keeps[i] == s.ntok) continue;
+      const size_t nblk = static_cast<size_t>(bm->blocks_of(keeps[i]));
+      for (size_t j = 0; j < nblk; ++j)
+        if (bm->ref[s.blocks[j]] > 1) left.push_back(s.blocks[j]);
+      left.insert(left.end(), s.blocks.begin() + nblk, s.blocks.end());
+    }
+    for (int32_t i = 0; i < n; ++i) {
+      Seq& s = *of[i];
+      if (keeps[i] == s.ntok) continue;
+      const size_t nblk = static_cast<size_t>(bm->blocks_of(keeps[i]));
+      for (size_t j = 0; j < nblk; ++j) {
+        const int32_t b = s.blocks[j];
+        if (bm->ref[b] > 1) {
+          s.blocks[j] = bm->take();
+        } else if (bm->hashed[b]) {
+          auto h = bm->by_hash.find(bm->block_hash[b]);
+          if (h != bm->by_hash.end() && h->second == b) bm->by_hash.erase(h);
+          bm->hashed[b] = 0;
+          bm->block_tokens[b].clear();
+        }
+      }
+      s.blocks.resize(nblk);
+      s.ntok = keeps[i];
+      s.hashing = false;
+      s.tail.clear();
+    }
+    for (int32_t b : left) bm->drop(b);
+    for (int32_t i = 0; i < n; ++i)
+      for (int32_t j = 0; j < width; ++j)
+        tables_out[static_cast<int64_t>(i) * width + j] =
+            j < bm->blocks_of(keeps[i]) ? of[i]->blocks[j] : -1;
+  } catch (const std::bad_alloc&) {
+    return PA_BM_NO_SPACE;
+  }
+  return 0;
+}
+
 int32_t pa_bm_evict(pa_block_manager* bm, int64_t seq, int64_t keep, int32_t* table_out,
                     int32_t cap) {
-  if (!bm || keep < 0 || cap < 0 || (cap > 0 && !table_out)) return PA_BM_BAD_ARG;
-  auto it = bm->seqs.find(seq);
-  if (it == bm->seqs.end() || keep > it->second.ntok) return PA_BM_BAD_ARG;
-  Seq& s = it->second;
-  const int64_t nblk = (keep + bm->bs - 1) / bm->bs;
-  if (nblk > cap) return PA_BM_BAD_ARG;
-  if (keep < s.ntok) {
-    int32_t shared = 0;
-    for (int64_t i = 0; i < nblk; ++i) shared += bm->ref[s.blocks[i]] > 1;
-    // fresh blocks come first: the released ones still hold keys that are to be moved
-    if (shared > bm->available()) return PA_BM_NO_SPACE;
-    for (int64_t i = 0; i < nblk; ++i) {
-      const int32_t b = s.blocks[i];
-      if (bm->ref[b] > 1) {
-        s.blocks[i] = bm->take();
-        bm->drop(b);
-      } else if (bm->hashed[b]) {
-        auto h = bm->by_hash.find(bm->block_hash[b]);
-        if (h != bm->by_hash.end() && h->second == b) bm->by_hash.erase(h);
-        bm->hashed[b] = 0;
-        bm->block_tokens[b].clear();
-      }
-    }
-    for (size_t i = static_cast<size_t>(nblk); i < s.blocks.size(); ++i) bm->drop(s.blocks[i]);
-    s.blocks.resize(static_cast<size_t>(nblk));
-    s.ntok = keep;
-    s.hashing = false;
-    s.tail.clear();
-  }
-  for (int64_t i = 0; i < cap; ++i) table_out[i] = i < nblk ? s.blocks[i] : -1;
-  return static_cast<int32_t>(nblk);
+  const int32_t rc = pa_bm_evict_batch(bm, &seq, &keep, 1, table_out, cap);
+  return rc < 0 ? rc : static_cast<int32_t>(bm->blocks_of(keep));
 }
 
 int32_t pa_bm_block_table(const pa_block_manager* bm, int64_t seq, int32_t* table_out,

@@ -1,5 +1,5 @@
 """Edges of the operators that shrink the cache, on the GPU, against the definitions in 64 bits: the
-smallest scales of MXFP4 pools.
+smallest scales of MXFP4 pools, and sequences evicted in one call.
 
 Tolerances are those of test_gpu_cache_shrinking.py (a score off by less than 2e-4 in the log2 domain,
 so a weight or a log-sum-exp's power by 4e-4; MXFP4 attention rounds a probability to f16, 2^-12);
@@ -9,7 +9,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_cache_shrinking import BS, Case, bits_f64, check_weights, mx_inputs
+from test_gpu_cache_shrinking import (BS, Case, bits_f64, check_weights, evict_reference, mx_inputs,
+                                      tile_rows)
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +105,42 @@ def test_mxfp4_attention_over_the_smallest_scales(which, d, hq, hkv, qlens):
     assert np.abs(got - ref).max() <= (2.0 ** -12 + 4e-4) * top + 8 * 2.0 ** -149
     assert np.abs(ref).max() > 0.1 * top
     check_weights(c, before, W.cpu().numpy(), list(range(4)), 1.0)
+
+
+# ---------------------------------------------------------------------------------------------
+# several sequences evicted in one call
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("mxfp4", 64)])
+def test_forks_and_neighbours_evicted_in_one_call(kind, d):
+    """A parent, its two forks and a sequence of its own, planned by one evict_batch call: what each
+    keeps is what it would keep alone, and a fork that stays out of the call keeps its keys."""
+    import paged_kv_cache_286_gb300 as pa
+    from paged_kv_cache_286_gb300.block_manager import BlockManager
+    hkv, L, keep, recent = 3, 1500, [600, 333, 1499, 40], 17
+    bm = BlockManager(340)
+    bm.append(0, L)
+    for s in (1, 2, 4):
+        bm.fork(0, s)
+    bm.append(3, 700)
+    seqs = [0, 1, 2, 3]
+    lens = [bm.num_tokens(s) for s in seqs]
+    width = -(-L // BS)
+    c = Case([L], [1], hkv, hkv, d, kind, seed=5, spare=340 - width)
+    c.tables = bm.tables(seqs + [4], width)
+    k0, v0 = (tile_rows(p, kind, d) for p in (c.k, c.v))
+    W0 = np.random.default_rng(6).random((4, hkv, L)).astype(np.float32)
+    dst = bm.evict_batch(seqs, keep, width)
+    want = evict_reference(c, W0, np.array(lens), np.array(keep), recent, 1499, dst, seqs, seqs)
+    cu = lambda x, t=np.int32: torch.from_numpy(np.ascontiguousarray(x, t)).cuda()  # noqa: E731
+    W = torch.from_numpy(W0).cuda()
+    ws = pa.new_workspace(pa.evict_workspace_size(4, hkv, L, 1499))
+    kept, new = pa.evict_keys(c.k, c.v, cu(c.tables[:4]), cu(lens), cu(keep), W, ws, max_context_len=L,
+                              max_keep_len=1499, recent=recent, dst_tables=cu(dst))
+    assert pa.check_error(ws) == 0
+    assert np.array_equal(kept.cpu().numpy(), want[0]) and new.tolist() == keep
+    assert np.array_equal(W.cpu().numpy(), want[4])
+    k1, v1 = (tile_rows(p, kind, d) for p in (c.k, c.v))
+    assert np.array_equal(k1, want[2]) and np.array_equal(v1, want[3])
+    still = c.tables[4]
+    assert bm.block_table(4).tolist() == still.tolist()
+    assert np.array_equal(k1[still], k0[still]) and np.array_equal(v1[still], v0[still])
