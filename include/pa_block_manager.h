@@ -89,7 +89,7 @@ int32_t pa_bm_free(pa_block_manager* bm, int64_t seq);
  * as block_tables they are pa_evict_keys' dst_tables.  Released blocks may be handed out by the
  * next call, so pa_evict_keys must be launched before, on the same stream as, whatever writes
  * those: another pa_evict_keys for tables of a later call among them.  Tokens appended later carry
- * no hash.
+ * no hash, and no cached prefix is taken for them.
  * Returns 0, PA_BM_NO_SPACE, or PA_BM_BAD_ARG (unknown sequence or one named twice, keeps[i] < 0 or
  * above its tokens, width too small). */
 int32_t pa_bm_evict_batch(pa_block_manager* bm, const int64_t* seqs, const int64_t* keeps, int32_t n,

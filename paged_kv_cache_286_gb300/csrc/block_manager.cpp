@@ -115,10 +115,11 @@ struct pa_block_manager {
     Seq scratch;
     Seq& s = fresh ? scratch : found->second;
 
-    // leading cached blocks (only for a sequence with no tokens yet, tokens known)
+    // leading cached blocks (only for a sequence with no tokens yet, tokens known; one evicted to
+    // nothing has had tokens)
     std::vector<int32_t> hits;
     std::vector<uint64_t> hit_hash;
-    if (tokens && s.ntok == 0) {
+    if (tokens && s.ntok == 0 && s.hashing) {
       uint64_t parent = s.chain;
       for (int32_t off = 0; off + bs <= n; off += bs) {
         uint64_t h;

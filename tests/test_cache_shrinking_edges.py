@@ -155,3 +155,21 @@ def test_batch_refusals_change_nothing():
         b = list(a)
         b[i] = bad
         assert L.pa_bm_evict_batch(ctypes.c_void_p(bm._h), *b) == -2
+
+
+# ---- after an eviction to nothing ----------------------------------------------------------------
+def test_a_sequence_evicted_to_nothing_takes_no_cached_prefix():
+    """Its next tokens follow those it dropped: blocks that hold the same tokens after the same prefix
+    were computed over that prefix's keys, and blocks of a fresh prompt at other positions."""
+    bm = manager(12)
+    toks = list(range(48))
+    bm.append_tokens(0, toks)                           # caches three blocks
+    bm.append_tokens(1, toks[:16])
+    bm.evict(1, 0)
+    slots, pairs, hit = bm.append_tokens(1, toks[16:48])
+    assert hit == 0 and len(slots) == 32 and pairs == []
+    assert not set(bm.block_table(1).tolist()) & set(bm.block_table(0).tolist())
+    bm.evict(1, 0)
+    assert bm.append_tokens(1, toks)[2] == 0
+    bm.append_tokens(2, toks)                           # an empty one still does
+    assert bm.block_table(2).tolist() == bm.block_table(0).tolist()
