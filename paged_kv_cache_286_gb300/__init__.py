@@ -166,6 +166,7 @@ def _step_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
                max_context_len, max_query_len, out, out_dtype, k_scale, v_scale):
     """Checks one step's tensors; returns its output and the C arguments up to out_dtype."""
     _need_caches(k_cache, v_cache)
+    _same_shape(k_cache, v_cache)
     _need(block_tables, "block_tables", (torch.int32,), 2)
     _need(context_lens, "context_lens", (torch.int32,), 1)
     _need(query_start_loc, "query_start_loc", (torch.int32,), 1)
@@ -240,7 +241,6 @@ def attention_key_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     its group.  weight_rows [num_seqs] (int32): the row of each sequence (None: row s)."""
     _need(q, "q", (torch.bfloat16,), 3)
     _need_caches(k_cache, v_cache)
-    _same_shape(k_cache, v_cache)
     _need(context_lens, "context_lens", (torch.int32,), 1)
     _need_weights(key_weights, k_cache.size(1), context_lens.size(0), weight_rows=weight_rows)
     with _on(stream, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, key_weights,
