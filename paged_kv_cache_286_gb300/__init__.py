@@ -119,6 +119,24 @@ def new_workspace(nbytes: int, device="cuda") -> torch.Tensor:
     return ws
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream, *tensors):
+    """Checks that the tensors (None: absent) share one device and returns a context in which the
+    call's allocations and its launch are on that device and on `stream` (None: the device's
+    current stream)."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {t.device} and {tensors[0].device}")
+    if stream is None:
+        return _HERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream of {stream.device} for tensors on {tensors[0].device}")
+    return torch.cuda.stream(stream)
+
+
 def cache_append(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
                  k_cache: torch.Tensor, v_cache: torch.Tensor, workspace: torch.Tensor, *,
                  k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
@@ -132,10 +150,10 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
     if k.shape != v.shape or k.shape[0] != slot_mapping.shape[0] or \
             k.shape[1:] != (desc.num_kv_heads, desc.head_dim):
         raise ValueError("k/v/slot_mapping shapes do not match the cache")
-    L = _lib.load()
-    _lib.check(L.pa_cache_append(_ptr(k), _ptr(v), _ptr(slot_mapping), k.shape[0],
-                                 _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc),
-                                 _ptr(workspace), _stream(stream)))
+    with _on(stream, k, v, slot_mapping, k_cache, v_cache, workspace):
+        _lib.check(_lib.load().pa_cache_append(
+            _ptr(k), _ptr(v), _ptr(slot_mapping), k.shape[0], _ptr(k_cache), _ptr(v_cache),
+            ctypes.byref(desc), _ptr(workspace), _stream(stream)))
 
 
 def attention_workspace_size(num_seqs: int, num_q_tokens: int, num_q_heads: int,
@@ -154,11 +172,12 @@ def attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
               v_scale: float = 1.0, stream=None) -> torch.Tensor:
     """Ragged paged attention: q [T, Hq, D] bf16 -> out [T, Hq, D] (fp32 or bf16)."""
     _need(q, "q", (torch.bfloat16,), 3)
-    out, args = _step_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
-                           workspace, scale, max_context_len, max_query_len, out, out_dtype,
-                           k_scale, v_scale)
-    _lib.check(_lib.load().pa_attention(*args, _ptr(workspace), workspace.numel(),
-                                        _stream(stream)))
+    with _on(stream, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, workspace, out):
+        out, args = _step_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                               workspace, scale, max_context_len, max_query_len, out, out_dtype,
+                               k_scale, v_scale)
+        _lib.check(_lib.load().pa_attention(*args, _ptr(workspace), workspace.numel(),
+                                            _stream(stream)))
     return out
 
 
@@ -189,24 +208,6 @@ def _step_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
         _ptr(q), T, _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc), _ptr(block_tables),
         block_tables.size(1), _ptr(context_lens), _ptr(query_start_loc), S,
         int(max_context_len), int(max_query_len), Hq, Hkv, D, float(scale), _ptr(out), odt)
-
-
-_HERE = contextlib.nullcontext()
-
-
-def _on(stream, *tensors):
-    """Checks that the tensors (None: absent) share one device and returns a context in which the
-    call's allocations and its launch are on that device and on `stream` (None: the device's
-    current stream)."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on different devices: {t.device} and {tensors[0].device}")
-    if stream is None:
-        return _HERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
-    if stream.device_index != dev:
-        raise ValueError(f"stream of {stream.device} for tensors on {tensors[0].device}")
-    return torch.cuda.stream(stream)
 
 
 def _need_weights(key_weights, num_kv_heads, num_seqs, **rows):
@@ -339,7 +340,8 @@ def cache_read(slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
 def check_error(workspace: torch.Tensor, stream=None, raise_on_error: bool = True) -> int:
     """Synchronise, read and clear the device error word; returns its PA_DEVERR_* bits."""
     word = ctypes.c_uint32(0)
-    st = _lib.load().pa_check_error(_ptr(workspace), _stream(stream), ctypes.byref(word))
+    with _on(stream, workspace):
+        st = _lib.load().pa_check_error(_ptr(workspace), _stream(stream), ctypes.byref(word))
     if raise_on_error and st != _lib.PA_OK:
         raise _lib.PagedAttnError(st, _lib.load().pa_last_error_string().decode())
     return int(word.value)
