@@ -315,8 +315,9 @@ __global__ void __cluster_dims__(kKwCluster, 1, 1) __launch_bounds__(kKwWarps * 
         }
         const float2 lse = *reinterpret_cast<const float2*>(&s_lse[buf][rt + 2 * qc]);
         // rows that do not see a key add nothing to it; every row sees the warp's keys if the
-        // tile's first does
-        if (key_w + 31 <= L - n + first_tok + div_g(r0 + rt)) {
+        // tile's first does.  (Rows that the run does not fill take the other way: they are zeros, but
+        // zero times a key's infinity is NaN.)
+        if (rt + 8 <= nr && key_w + 31 <= L - n + first_tok + div_g(r0 + rt)) {
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll

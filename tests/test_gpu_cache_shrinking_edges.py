@@ -1,5 +1,5 @@
 """Edges of the operators that shrink the cache, on the GPU, against the definitions in 64 bits: the
-smallest scales of MXFP4 pools, and sequences evicted in one call.
+smallest scales of MXFP4 pools, sequences evicted in one call, and keys that hold infinities.
 
 Tolerances are those of test_gpu_cache_shrinking.py (a score off by less than 2e-4 in the log2 domain,
 so a weight or a log-sum-exp's power by 4e-4; MXFP4 attention rounds a probability to f16, 2^-12);
@@ -144,3 +144,32 @@ def test_forks_and_neighbours_evicted_in_one_call(kind, d):
     still = c.tables[4]
     assert bm.block_table(4).tolist() == still.tolist()
     assert np.array_equal(k1[still], k0[still]) and np.array_equal(v1[still], v0[still])
+
+
+# ---------------------------------------------------------------------------------------------
+# keys that hold infinities
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("d,hq,hkv,ctx,qlens", [
+    (128, 1, 1, [300, 40], [37, 1]), (64, 6, 2, [300, 40], [45, 2]), (128, 3, 3, [513, 70], [33, 5]),  # mma.sync
+    (128, 16, 16, [1300, 900], [201, 70]), (64, 16, 16, [1300, 900], [201, 1]),                     # tcgen05
+])
+def test_key_weights_of_keys_with_infinities(d, hq, hkv, ctx, qlens):
+    """A key whose scores are all minus infinity receives nothing: decay * W, whatever the rows of the
+    last tile that no query fills."""
+    import paged_kv_cache_286_gb300 as pa
+    c = Case(ctx, qlens, hq, hkv, d, "bf16", seed=d + hq)
+    c.q[..., 3] = -c.q[..., 3].abs() - 0.5
+    at = [0, 5, ctx[0] - qlens[0]]                                   # seen by every query of the first run
+    for j in at:
+        c.k[int(c.tables[0, j // BS]), :, j % BS, 3] = float("inf")
+        c.kv[int(c.tables[0, j // BS]), :, j % BS, 3] = np.inf
+    t, cl, qsl = c.dev()
+    before = np.random.default_rng(2).random((2, hkv, max(ctx))).astype(np.float32)
+    W = torch.from_numpy(before).cuda()
+    ws = c.workspace(pa, True)
+    ws[256:] = 0xFF
+    out = pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, cl, qsl, W, ws, decay=0.5, **c.hints())
+    assert pa.check_error(ws) == 0
+    assert torch.isfinite(out).all()
+    check_weights(c, before, W.cpu().numpy(), [0, 1], 0.5)
+    assert np.array_equal(W[0][:, at].cpu().numpy(), before[0][:, at] / 2)
