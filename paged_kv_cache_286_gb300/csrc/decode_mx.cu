@@ -190,9 +190,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, MxCfg<D, RT, HPI>::kCtas)
     }
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // power of two e with amax * 2^e < 2^15 (f16 range), exact scaling
-    const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 126;
-    const int e = max(-100, min(100, 15 - ex));
+    // power of two e with amax * 2^e < 2^15 (f16 range), exact scaling; both 2^e and 2^-e are normal
+    const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 126;  // -126 .. 129
+    const int e = min(126, 15 - ex);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {

@@ -1,5 +1,6 @@
 """Edges of the operators that shrink the cache, on the GPU, against the definitions in 64 bits: the
-smallest scales of MXFP4 pools, sequences evicted in one call, and keys that hold infinities.
+smallest scales of MXFP4 pools, sequences evicted in one call, keys that hold infinities, and queries of any
+size.
 
 Tolerances are those of test_gpu_cache_shrinking.py (a score off by less than 2e-4 in the log2 domain,
 so a weight or a log-sum-exp's power by 4e-4; MXFP4 attention rounds a probability to f16, 2^-12);
@@ -173,3 +174,22 @@ def test_key_weights_of_keys_with_infinities(d, hq, hkv, ctx, qlens):
     assert torch.isfinite(out).all()
     check_weights(c, before, W.cpu().numpy(), [0, 1], 0.5)
     assert np.array_equal(W[0][:, at].cpu().numpy(), before[0][:, at] / 2)
+
+
+# ---------------------------------------------------------------------------------------------
+# queries of any size over MXFP4 keys
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("hq,hkv,qlens", [(4, 4, (1, 1, 1)), (8, 2, (1, 3, 2)), (16, 1, (2, 1, 1))])
+@pytest.mark.parametrize("size", [120, -120])
+def test_mxfp4_queries_of_any_size(hq, hkv, qlens, size):
+    """q of 2^120 and 2^-120, the scale in proportion: scores, and so outputs, of the usual size."""
+    import paged_kv_cache_286_gb300 as pa
+    c = Case([300, 33, 90], qlens, hq, hkv, 128, "mxfp4", seed=hq)
+    c.q = (c.q.float() * 2.0 ** size).bfloat16()
+    c.scale *= 2.0 ** -size
+    t, ctx, qsl = c.dev()
+    ws = c.workspace(pa)
+    ref = c.reference()[0]
+    out = pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, **c.hints())
+    assert pa.check_error(ws) == 0
+    assert np.abs(bits_f64(out) - ref).max() <= (2.0 ** -12 + 4e-4) * np.abs(c.vv).max()
