@@ -214,7 +214,11 @@ size_t pa_attention_key_weights_workspace_size(int32_t num_seqs, int32_t num_q_t
  *   decay         >= 0; 1 sums over all steps.
  * The other arguments, the output and the errors are pa_attention's (a sequence that it skips
  * accumulates nothing; nor does a key in a block outside the pool).  The sums are fp32 and their
- * order is fixed: the same call gives the same bits. */
+ * order is fixed: the same call gives the same bits.
+ * If a wait of the attention runs out (PA_DEVERR_TIMEOUT), the weights stay as they are, and so they
+ * do in later calls until pa_check_error has cleared the error word.  If a wait of the accumulation
+ * itself runs out, some of the step's keys have their sums and others do not: the rows of its
+ * sequences are lost, and the caller zeroes them. */
 pa_status pa_attention_key_weights(
     const void* q, int32_t num_q_tokens, const void* k_cache, const void* v_cache,
     const pa_cache_desc* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
@@ -346,8 +350,9 @@ void pa_set_wait_limit_ns(uint64_t ns);
  * launches (the first copy of the first work item claimed) while that copy's barrier still
  * expects the bytes, so that the bounded waits on it expire and the call ends with
  * PA_ERR_TIMEOUT without any fault: the expiry and drain paths of the kernels can be exercised
- * on a real GPU.  pa_attention_key_weights' tensor-core kernel does the same over bf16 pools.  (The
- * split-KV kernel of MXFP4 pools has no wait that could run out and ignores the hook.) */
+ * on a real GPU.  2 leaves the attention kernels whole and does the same in
+ * pa_attention_key_weights' tensor-core kernel over bf16 pools.  (The split-KV kernel of MXFP4 pools
+ * has no wait that could run out and ignores the hook.) */
 void pa_test_skip_one_copy(int32_t enable);
 
 /* Self-test of the bounded wait: one thread waits, for limit_ns (in (0, 10 s]), on an mbarrier

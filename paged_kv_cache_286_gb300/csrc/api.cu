@@ -368,7 +368,7 @@ void pa_set_kernel_span_buffer(uint64_t* device_buffer) { g_span = device_buffer
 
 void pa_set_wait_limit_ns(uint64_t ns) { g_wait_ns = ns ? ns : pa::kWaitLimitNs; }
 
-void pa_test_skip_one_copy(int32_t enable) { g_skip_copy = enable ? 1 : 0; }
+void pa_test_skip_one_copy(int32_t enable) { g_skip_copy = enable == 2 ? 2 : enable ? 1 : 0; }
 
 pa_status pa_workspace_init(void* workspace, cudaStream_t stream) {
   g_last_error.clear();
@@ -564,7 +564,7 @@ static pa_status attend(const void* q, int32_t num_q_tokens, const void* k_cache
   a.pf_before = g_pf_before;
   a.pf_after = g_pf_after;
   a.wait_ns = g_wait_ns;
-  a.skip_copy = g_skip_copy;
+  a.skip_copy = g_skip_copy == 1;
   a.span = g_span;
   a.lse = lse;
   a.scores = scores.data;
@@ -669,7 +669,7 @@ pa_status pa_attention_key_weights(
       scale * 1.4426950408889634f * (cache->cache_dtype == PA_FP8_E4M3 ? cache->k_scale : 1.f);
   a.decay = decay;
   a.wait_ns = g_wait_ns;
-  a.skip_copy = g_skip_copy;
+  a.skip_copy = g_skip_copy == 2;
   // Long runs go to the tensor-core kernel if their key chunks, one to a CTA, fill at least half the
   // SMs; with fewer, four CTAs to a chunk of the other kernel end sooner.  (8 kv heads, E4M3, 32 q
   // heads: a run of 512 tokens in 1,280 keys, 40 chunks, 31 us here and 29 there; in 2,560 keys 32

@@ -39,6 +39,13 @@ constexpr int kKwRows = 64;     // rows staged in shared memory at a time
 constexpr int kKwCluster = 4;   // CTAs that share an item's rows
 
 
+// Whether a wait of the attention before has run out (in this call, or in an earlier one whose error
+// nobody has read): its log-sum-exps and scores are not all there, and the weights, which last over
+// steps, stay as they are.
+__device__ __forceinline__ bool kw_timed_out(const KeyWeightsArgs& a) {
+  return *a.err & PA_DEVERR_TIMEOUT;
+}
+
 // Whether a sequence accumulates weights in this step.
 __device__ __forceinline__ bool kw_accumulates(const KeyWeightsArgs& a, int s,
                                                uint32_t* err_bits) {
@@ -68,13 +75,16 @@ __device__ __forceinline__ int kw_chunks(const KeyWeightsArgs& a, int s, uint32_
 // L2's) and by launch.
 constexpr int kFinThreads = 256;
 constexpr int kFinShare = 4096;  // keys of a share at least (of the longest sequence)
+template <bool kBeside>
 __device__ __forceinline__ void finish_share(const KeyWeightsArgs& a) {
   __shared__ float s_lse[kDecodeMaxRows];
   const int s = blockIdx.x, h = blockIdx.y;
   uint32_t bits = 0;
+  const bool lost = kw_timed_out(a);
   const bool ok = kw_accumulates(a, s, &bits);
   if (bits && threadIdx.x == 0) set_error(a.err, bits);
-  if (!ok) return;
+  // (beside the tensor-core kernel, which may set the bit meanwhile: one answer for the CTA)
+  if (kBeside ? __syncthreads_or(!ok || lost) : !ok || lost) return;
   const int t0 = a.qsl[s], n = a.qsl[s + 1] - t0, L = a.context_lens[s];
   const int G = a.num_q_heads / a.num_kv_heads;
   if (n * G > a.score_rows || (blockIdx.z && blockIdx.z * kFinShare >= L)) return;
@@ -141,7 +151,7 @@ template <bool kBeside>
 __global__ void __launch_bounds__(kFinThreads, kBeside ? 6 : 5)
     kw_finish_kernel(const KeyWeightsArgs a) {
   if (!kBeside) grid_dependency_wait();
-  finish_share(a);
+  finish_share<kBeside>(a);
   if (kBeside) grid_dependency_wait();
 }
 
@@ -152,9 +162,10 @@ __global__ void __launch_bounds__(1024) kw_plan_kernel(const KeyWeightsArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int carry = 0;
   uint32_t bits = 0;
+  const bool lost = __syncthreads_or(kw_timed_out(a));  // then there are no items
   for (int base = 0; base < a.num_seqs; base += 1024) {
     const int s = base + tid;
-    const int c = s < a.num_seqs ? kw_chunks(a, s, &bits) : 0;
+    const int c = s < a.num_seqs && !lost ? kw_chunks(a, s, &bits) : 0;
     int x = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

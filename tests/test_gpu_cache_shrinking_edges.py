@@ -1,6 +1,6 @@
 """Edges of the operators that shrink the cache, on the GPU, against the definitions in 64 bits: the
-smallest scales of MXFP4 pools, sequences evicted in one call, keys that hold infinities, and queries of any
-size.
+smallest scales of MXFP4 pools, sequences evicted in one call, keys that hold infinities, queries of any
+size, and waits that run out.
 
 Tolerances are those of test_gpu_cache_shrinking.py (a score off by less than 2e-4 in the log2 domain,
 so a weight or a log-sum-exp's power by 4e-4; MXFP4 attention rounds a probability to f16, 2^-12);
@@ -193,3 +193,64 @@ def test_mxfp4_queries_of_any_size(hq, hkv, qlens, size):
     out = pa.attention(c.q.cuda(), c.k, c.v, t, ctx, qsl, ws, **c.hints())
     assert pa.check_error(ws) == 0
     assert np.abs(bits_f64(out) - ref).max() <= (2.0 ** -12 + 4e-4) * np.abs(c.vv).max()
+
+
+# ---------------------------------------------------------------------------------------------
+# waits that run out
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("d,hq,hkv,ctx,qlens", [
+    (128, 8, 2, [500, 70], [1, 1]), (64, 4, 4, [500, 70], [1, 2]),           # decode tokens
+    (128, 8, 2, [500, 700], [1, 60]), (64, 16, 16, [1300, 500], [200, 1]),   # both passes over K
+])
+def test_weights_stay_as_they_are_when_the_attention_times_out(d, hq, hkv, ctx, qlens):
+    import paged_kv_cache_286_gb300 as pa
+    c = Case(ctx, qlens, hq, hkv, d, "bf16", seed=3)
+    t, cl, qsl = c.dev()
+    L, ws = pa.library(), c.workspace(pa, True)
+    ws[256:] = 0xFF
+    before = torch.rand(2, hkv, max(ctx), device="cuda")
+    want, W = before.clone(), before.clone()
+    pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, cl, qsl, want, ws, **c.hints())
+    assert pa.check_error(ws) == 0
+    try:
+        L.pa_set_wait_limit_ns(20_000_000)
+        L.pa_test_skip_one_copy(1)
+        pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, cl, qsl, W, ws, **c.hints())
+        L.pa_test_skip_one_copy(0)
+        # a step behind it, before anyone has looked
+        pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, cl, qsl, W, ws, **c.hints())
+        assert pa.check_error(ws, raise_on_error=False) & 0x8
+    finally:
+        L.pa_test_skip_one_copy(0)
+        L.pa_set_wait_limit_ns(0)
+    assert torch.equal(W, before)
+    pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, cl, qsl, W, ws, **c.hints())
+    assert pa.check_error(ws) == 0 and torch.equal(W, want)
+
+
+@pytest.mark.parametrize("d,hq,hkv,ctx,qlens", [(128, 16, 16, [1300, 500], [200, 1]), (64, 16, 16, [1300, 900], [200, 77])])
+def test_a_wait_of_the_weights_themselves_that_runs_out(d, hq, hkv, ctx, qlens):
+    """The attention is done, the rows of the weights are lost, and the next call is whole again."""
+    import paged_kv_cache_286_gb300 as pa
+    c = Case(ctx, qlens, hq, hkv, d, "bf16", seed=3)
+    t, cl, qsl = c.dev()
+    L, ws = pa.library(), c.workspace(pa, True)
+    ws[256:] = 0xFF
+    W = torch.rand(3, hkv, max(ctx), device="cuda")
+    before = W.clone()
+    out = pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, cl, qsl, W, ws, **c.hints())
+    want = W.clone()
+    assert pa.check_error(ws) == 0
+    W.copy_(before)
+    try:
+        L.pa_set_wait_limit_ns(20_000_000)
+        L.pa_test_skip_one_copy(2)
+        again = pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, cl, qsl, W, ws, **c.hints())
+        assert pa.check_error(ws, raise_on_error=False) == 0x8
+    finally:
+        L.pa_test_skip_one_copy(0)
+        L.pa_set_wait_limit_ns(0)
+    assert torch.equal(again, out) and torch.equal(W[2], before[2])
+    W.copy_(before)
+    pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, cl, qsl, W, ws, **c.hints())
+    assert pa.check_error(ws) == 0 and torch.equal(W, want)
