@@ -225,7 +225,7 @@ class DeviceWorkload:
         self.copy_stream = torch.cuda.Stream(device)
         nbytes = pa.attention_workspace_size(w.num_seqs, w.num_tokens, w.num_q_heads,
                                              w.num_kv_heads, w.head_dim, w.max_context_len,
-                                             w.max_query_len)
+                                             w.max_query_len, k_cache=self.k_cache)
         self.ws = pa.new_workspace(nbytes, device)
         P = w.slot_prior.shape[0]
         for a in range(0, P, 1 << 16):   # set-up: the context cached before the step

@@ -149,12 +149,18 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const pa_cache_desc* cach
                          cudaStream_t stream);
 
 /* Workspace bytes pa_attention needs for a step of this shape (host-only, no device call).
- * max_context_len / max_query_len are upper bounds of context_lens[s] and n_s.  With runs of more
- * than 32 (token x q head) rows up to 256 MiB of it are for the bf16 copies that MXFP4 pools use
- * (see pa_attention); steps over other pools need not have them. */
+ * max_context_len / max_query_len are upper bounds of context_lens[s] and n_s. */
 size_t pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_tokens, int32_t num_q_heads,
                                    int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                    int32_t max_context_len, int32_t max_query_len);
+
+/* The same for a pool of the given cache_dtype, with what makes its steps fast: for PA_MXFP4 and runs
+ * of more than 32 (token x q head) rows up to 256 MiB more, for the bf16 copies that pa_attention then
+ * makes.  For other pools it is pa_attention_workspace_size. */
+size_t pa_attention_workspace_size_for(int32_t cache_dtype, int32_t num_seqs, int32_t num_q_tokens,
+                                       int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t block_size, int32_t max_context_len,
+                                       int32_t max_query_len);
 
 /* Ragged paged attention of one step.
  *   q             [num_q_tokens][num_q_heads][head_dim] bf16 (device).
@@ -177,9 +183,10 @@ size_t pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_tokens, int32
  * them, the split-KV kernel on the rest, and the merge of split sequences.
  * MXFP4 pools have their own split-KV kernel for runs of up to 32 (token x q head) rows.  The
  * sequences of longer runs are written out as bf16 into the end of the workspace and go to the
- * prefill tiles, if the heads allow those (128 divisible by the group, at most 8); a workspace that
- * holds the split-KV part but not all of that copy is accepted, and the split-KV kernel then also
- * takes the runs for whose sequences it has no room.
+ * prefill tiles, if the heads allow those (128 divisible by the group, at most 8); a workspace of
+ * pa_attention_workspace_size_for holds all of that copy (up to its limit); a smaller one, down to
+ * pa_attention_workspace_size, is accepted, and the split-KV kernel then also takes the runs for
+ * whose sequences it has no room.
  * Work enqueued on `stream` after the call sees all of it complete.  The call records no event
  * and creates no stream, so it can be captured into a CUDA graph like any kernel launch. */
 pa_status pa_attention(const void* q, int32_t num_q_tokens, const void* k_cache,
@@ -198,6 +205,13 @@ size_t pa_attention_key_weights_workspace_size(int32_t num_seqs, int32_t num_q_t
                                                int32_t num_q_heads, int32_t num_kv_heads,
                                                int32_t head_dim, int32_t block_size,
                                                int32_t max_context_len, int32_t max_query_len);
+
+/* The same for a pool of the given cache_dtype (see pa_attention_workspace_size_for). */
+size_t pa_attention_key_weights_workspace_size_for(int32_t cache_dtype, int32_t num_seqs,
+                                                   int32_t num_q_tokens, int32_t num_q_heads,
+                                                   int32_t num_kv_heads, int32_t head_dim,
+                                                   int32_t block_size, int32_t max_context_len,
+                                                   int32_t max_query_len);
 
 /* pa_attention that also accumulates how much attention every cached key received, the measure by
  * which pa_evict_keys chooses.  Of a sequence s with query tokens, for every kv head h and key j
@@ -281,9 +295,8 @@ pa_status pa_evict_keys(void* k_cache, void* v_cache, const pa_cache_desc* cache
  * path where an allocation could stall the device.  They can still pass inputs and outputs but
  * not a workspace, so this call uses a scratch array built into the library instead:
  * PA_NOALLOC_SCRATCH_BYTES per device, held by every GPU that loads the library until the
- * process exits.  A step whose pa_attention_workspace_size, less its part for MXFP4 copies, exceeds
- * it is rejected with PA_ERR_INVALID_ARG and a message; use pa_attention with a workspace for larger
- * steps.
+ * process exits.  A step whose pa_attention_workspace_size exceeds it is rejected with
+ * PA_ERR_INVALID_ARG and a message; use pa_attention with a workspace for larger steps.
  *   Arguments are those of pa_attention without workspace/workspace_bytes, plus
  *   error_word    optional DEVICE pointer (may be NULL) that receives, asynchronously on
  *                 `stream`, this call's PA_DEVERR_* bits (0 for a step with nothing to do).  It

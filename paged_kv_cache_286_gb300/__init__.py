@@ -6,7 +6,7 @@ step of the computation runs in the library's CUDA kernels; if the library is mi
 raise, there is no CPU fallback.
 
     import paged_kv_cache_286_gb300 as pa
-    ws = pa.new_workspace(pa.attention_workspace_size(...), device="cuda")
+    ws = pa.new_workspace(pa.attention_workspace_size(..., k_cache=k_cache), device="cuda")
     pa.cache_append(k, v, slot_mapping, k_cache, v_cache, ws)
     out = pa.attention(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, ws,
                        scale=..., max_context_len=..., max_query_len=...)
@@ -158,10 +158,14 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
 
 def attention_workspace_size(num_seqs: int, num_q_tokens: int, num_q_heads: int,
                              num_kv_heads: int, head_dim: int, max_context_len: int,
-                             max_query_len: int, block_size: int = 16) -> int:
-    return int(_lib.load().pa_attention_workspace_size(
-        num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
-        max_context_len, max_query_len))
+                             max_query_len: int, block_size: int = 16,
+                             k_cache: Optional[torch.Tensor] = None) -> int:
+    """Workspace bytes of a step of this shape over the pool `k_cache`.  Without one: enough for a
+    pool of any type, which with runs of more than 32 (token x q head) rows is up to 256 MiB more
+    than bf16 and E4M3 pools use."""
+    return int(_lib.load().pa_attention_workspace_size_for(
+        PA_MXFP4 if k_cache is None else cache_desc(k_cache).cache_dtype, num_seqs, num_q_tokens,
+        num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, max_query_len))
 
 
 def attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -223,10 +227,12 @@ def _need_weights(key_weights, num_kv_heads, num_seqs, **rows):
 
 def attention_key_weights_workspace_size(num_seqs: int, num_q_tokens: int, num_q_heads: int,
                                          num_kv_heads: int, head_dim: int, max_context_len: int,
-                                         max_query_len: int, block_size: int = 16) -> int:
-    return int(_lib.load().pa_attention_key_weights_workspace_size(
-        num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
-        max_context_len, max_query_len))
+                                         max_query_len: int, block_size: int = 16,
+                                         k_cache: Optional[torch.Tensor] = None) -> int:
+    """The same for attention_key_weights."""
+    return int(_lib.load().pa_attention_key_weights_workspace_size_for(
+        PA_MXFP4 if k_cache is None else cache_desc(k_cache).cache_dtype, num_seqs, num_q_tokens,
+        num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, max_query_len))
 
 
 def attention_key_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,

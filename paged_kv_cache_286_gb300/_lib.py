@@ -25,7 +25,8 @@ EXPORTED = ["pa_cache_append", "pa_attention_workspace_size", "pa_attention", "p
             "pa_attention_noalloc", "pa_copy_blocks", "pa_set_kernel_span_buffer",
             "pa_set_wait_limit_ns", "pa_attention_key_weights",
             "pa_attention_key_weights_workspace_size", "pa_evict_keys", "pa_evict_workspace_size",
-            "pa_cache_read",
+            "pa_cache_read", "pa_attention_workspace_size_for",
+            "pa_attention_key_weights_workspace_size_for",
             "pa_test_skip_one_copy", "pa_selftest_wait_timeout"]
 EXPORTED_BM = ["pa_bm_create", "pa_bm_destroy", "pa_bm_num_free", "pa_bm_append",
                "pa_bm_append_tokens", "pa_bm_fork", "pa_bm_free", "pa_bm_block_table",
@@ -70,6 +71,9 @@ def load() -> ctypes.CDLL:
     L.pa_attention.restype = ctypes.c_int
     L.pa_attention_key_weights_workspace_size.argtypes = [i32] * 8
     L.pa_attention_key_weights_workspace_size.restype = ctypes.c_size_t
+    for f in (L.pa_attention_workspace_size_for, L.pa_attention_key_weights_workspace_size_for):
+        f.argtypes = [i32] * 9
+        f.restype = ctypes.c_size_t
     L.pa_attention_key_weights.argtypes = [vp, i32, vp, vp, ctypes.POINTER(CacheDesc), i32p, i32,
                                            i32p, i32p, i32, i32, i32, i32, i32, i32,
                                            ctypes.c_float, vp, i32, vp, i32p, i32, i32,

@@ -454,9 +454,19 @@ size_t pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_tokens, int32
   (void)block_size;
   return pa::workspace_layout(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
                               max_context_len, max_query_len)
-             .total +
-         pa::mx_stage_bytes(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
-                            max_context_len, max_query_len);
+      .total;
+}
+
+size_t pa_attention_workspace_size_for(int32_t cache_dtype, int32_t num_seqs, int32_t num_q_tokens,
+                                       int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t block_size, int32_t max_context_len,
+                                       int32_t max_query_len) {
+  return pa_attention_workspace_size(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
+                                     block_size, max_context_len, max_query_len) +
+         (cache_dtype == PA_MXFP4
+              ? pa::mx_stage_bytes(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
+                                   max_context_len, max_query_len)
+              : 0);
 }
 
 struct Scores {  // where the split-KV path writes its scores (DecodeParams)
@@ -598,9 +608,21 @@ size_t pa_attention_key_weights_workspace_size(int32_t num_seqs, int32_t num_q_t
   (void)block_size;
   return pa::key_weights_layout(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
                                 max_context_len, max_query_len)
-             .total +
-         pa::mx_stage_bytes(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
-                            max_context_len, max_query_len);
+      .total;
+}
+
+size_t pa_attention_key_weights_workspace_size_for(int32_t cache_dtype, int32_t num_seqs,
+                                                   int32_t num_q_tokens, int32_t num_q_heads,
+                                                   int32_t num_kv_heads, int32_t head_dim,
+                                                   int32_t block_size, int32_t max_context_len,
+                                                   int32_t max_query_len) {
+  return pa_attention_key_weights_workspace_size(num_seqs, num_q_tokens, num_q_heads, num_kv_heads,
+                                                 head_dim, block_size, max_context_len,
+                                                 max_query_len) +
+         (cache_dtype == PA_MXFP4
+              ? pa::mx_stage_bytes(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_dim,
+                                   max_context_len, max_query_len)
+              : 0);
 }
 
 pa_status pa_attention_key_weights(

@@ -58,10 +58,10 @@ extern "C" pa_status pa_attention_noalloc(
     pa::set_last_error(msg);
     return PA_ERR_CUDA;
   }
-  // (without the area in which MXFP4 chunks are staged: they do with what is left)
-  const size_t need = pa::workspace_layout(num_seqs, num_q_tokens, num_q_heads, num_kv_heads,
-                                           head_dim, max_context_len, max_query_len)
-                          .total;
+  // (MXFP4 chunks are staged in what is left)
+  const size_t need = pa_attention_workspace_size(num_seqs, num_q_tokens, num_q_heads,
+                                                  num_kv_heads, head_dim, pa::kBlockSize,
+                                                  max_context_len, max_query_len);
   if (need > PA_NOALLOC_SCRATCH_BYTES) {
     char msg[256];
     snprintf(msg, sizeof(msg),

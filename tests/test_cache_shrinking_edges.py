@@ -173,3 +173,27 @@ def test_a_sequence_evicted_to_nothing_takes_no_cached_prefix():
     assert bm.append_tokens(1, toks)[2] == 0
     bm.append_tokens(2, toks)                           # an empty one still does
     assert bm.block_table(2).tolist() == bm.block_table(0).tolist()
+
+
+# ---- workspaces ----------------------------------------------------------------------------------
+def test_only_mxfp4_steps_have_room_for_bf16_copies():
+    """48 decode tokens beside two chunks of 512, 32 q heads on 8 of 128 dims, contexts to 4,096."""
+    torch = pytest.importorskip("torch")
+    import paged_kv_cache_286_gb300 as pa
+    L = pa.library()
+    shape, bs = (50, 48 + 2 * 512, 32, 8, 128), 16
+    BF16, E4M3, MXFP4 = 0, 1, 3
+    pools = {BF16: torch.zeros(4, 8, 16, 128, dtype=torch.bfloat16),
+             E4M3: torch.zeros(4, 8, 16, 128, dtype=torch.uint8), MXFP4: torch.zeros(4, 8, 1088, dtype=torch.uint8)}
+    for name in ("attention", "attention_key_weights"):
+        plain = getattr(L, f"pa_{name}_workspace_size")(*shape, bs, 4096, 512)
+        size_for = getattr(L, f"pa_{name}_workspace_size_for")
+        py = getattr(pa, f"{name}_workspace_size")
+        for dt in (BF16, E4M3):
+            assert size_for(dt, *shape, bs, 4096, 512) == plain == py(*shape, 4096, 512, k_cache=pools[dt])
+        mx = size_for(MXFP4, *shape, bs, 4096, 512)
+        assert (256 << 20) <= mx - plain <= (257 << 20)
+        assert mx == py(*shape, 4096, 512) == py(*shape, 4096, 512, k_cache=pools[MXFP4])
+        # decode steps have none of it
+        assert size_for(MXFP4, 50, 50, 32, 8, 128, bs, 4096, 1) == \
+            getattr(L, f"pa_{name}_workspace_size")(50, 50, 32, 8, 128, bs, 4096, 1)
