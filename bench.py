@@ -301,12 +301,12 @@ class DeviceWorkload:
         w = self.w
         size = self.pa.attention_workspace_size(w.num_seqs, w.num_tokens, w.num_q_heads,
                                                 w.num_kv_heads, w.head_dim, w.max_context_len,
-                                                w.max_query_len)
+                                                w.max_query_len, k_cache=self.k_cache)
 
         def up(x):
             return (x + 255) // 256 * 256
-        # the header and the four per-sequence arrays: more means split partials
-        no_partials = 256 + 3 * up(4 * (w.num_seqs + 1)) + up(4 * max(w.num_seqs, 1))
+        # the header and the five per-sequence arrays: more means split partials
+        no_partials = 256 + 3 * up(4 * (w.num_seqs + 1)) + 2 * up(4 * max(w.num_seqs, 1))
         return 3 + (1 if size > no_partials else 0) + (1 if self.has_prefill() else 0)
 
 
