@@ -11,6 +11,7 @@
 #include <mutex>
 #include <string>
 
+#include "launch_cache.h"
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
@@ -272,23 +273,11 @@ KeyWeightsLayout key_weights_layout(int32_t S, int32_t T, int32_t Hq, int32_t Hk
 }
 
 cudaError_t launch_info_impl(const void* kern, int threads, int smem_bytes, LaunchInfo* out) {
-  struct Entry {
-    const void* kern;
-    int dev;
-    LaunchInfo info;
-  };
-  static std::mutex mu;
-  static Entry table[64];
-  static int used = 0;
+  static LaunchCache<LaunchInfo> cache;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < used; ++i)
-    if (table[i].kern == kern && table[i].dev == dev) {
-      *out = table[i].info;
-      return cudaSuccess;
-    }
+  if (cache.find(kern, dev, out)) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
   if (e != cudaSuccess) return e;
   LaunchInfo li;
@@ -297,7 +286,7 @@ cudaError_t launch_info_impl(const void* kern, int threads, int smem_bytes, Laun
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&li.per_sm, kern, threads, smem_bytes);
   if (e != cudaSuccess) return e;
   if (li.per_sm < 1) li.per_sm = 1;
-  if (used < 64) table[used++] = Entry{kern, dev, li};
+  cache.put(kern, dev, li);
   *out = li;
   return cudaSuccess;
 }
