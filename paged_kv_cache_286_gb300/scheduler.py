@@ -20,6 +20,10 @@ context_lens and block tables.
 Request model: `prompt_len` prompt tokens, then `output_len` generated tokens.  The step that
 completes the prompt yields the first token; each later step appends the previous token and
 yields the next.  A preempted request recomputes its prompt and the tokens it had generated.
+
+A request's context is its tokens: every one of them has its keys in the cache.  So the scheduler does
+not go together with eviction of keys (BlockManager.evict of a request it runs, after which positions
+and lengths are no longer counts of tokens); a step after one raises RuntimeError.
 """
 
 from __future__ import annotations
@@ -128,6 +132,10 @@ class Scheduler:
         return slots
 
     def step(self) -> Optional[StepBatch]:
+        for r in self.running:
+            if r.computed and self.bm.num_tokens(r.rid) != r.computed:
+                raise RuntimeError(f"request {r.rid} has {self.bm.num_tokens(r.rid)} keys for {r.computed} "
+                                   "tokens: the scheduler does not plan over evicted keys")
         self.step_no += 1
         t = self.step_no
         budget = self.token_budget

@@ -197,3 +197,19 @@ def test_only_mxfp4_steps_have_room_for_bf16_copies():
         # decode steps have none of it
         assert size_for(MXFP4, 50, 50, 32, 8, 128, bs, 4096, 1) == \
             getattr(L, f"pa_{name}_workspace_size")(50, 50, 32, 8, 128, bs, 4096, 1)
+
+
+# ---- the scheduler -------------------------------------------------------------------------------
+@pytest.mark.parametrize("prefix", [False, True])
+def test_scheduler_refuses_to_plan_over_evicted_keys(prefix):
+    """Its context lengths and slots count tokens."""
+    from paged_kv_cache_286_gb300.scheduler import Request, Scheduler
+    s = Scheduler(16, prefix_caching=prefix)
+    s.submit(Request(0, 40, 8))
+    s.submit(Request(1, 20, 8))
+    for _ in range(3):
+        assert s.step() is not None
+    s.bm.evict(1, 20)
+    with pytest.raises(RuntimeError, match="evicted"):
+        s.step()
+    assert s.step_no == 3
