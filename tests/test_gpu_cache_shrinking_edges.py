@@ -1,6 +1,6 @@
 """Edges of the operators that shrink the cache, on the GPU, against the definitions in 64 bits: the
 smallest scales of MXFP4 pools, sequences evicted in one call, keys that hold infinities, queries of any
-size, and waits that run out.
+size, waits that run out, and key weights that start from nothing.
 
 Tolerances are those of test_gpu_cache_shrinking.py (a score off by less than 2e-4 in the log2 domain,
 so a weight or a log-sum-exp's power by 4e-4; MXFP4 attention rounds a probability to f16, 2^-12);
@@ -254,3 +254,25 @@ def test_a_wait_of_the_weights_themselves_that_runs_out(d, hq, hkv, ctx, qlens):
     W.copy_(before)
     pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, cl, qsl, W, ws, **c.hints())
     assert pa.check_error(ws) == 0 and torch.equal(W, want)
+
+
+# ---------------------------------------------------------------------------------------------
+# key weights that start from nothing
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("bf16", 64), ("e4m3", 128), ("mxfp4", 128), ("mxfp4", 64)])
+@pytest.mark.parametrize("qlens,ctx,hq,hkv", [
+    ([1] * 6, [1, 17, 100, 513, 2000, 5000], 8, 2), ([1] * 4, [33, 1000, 16, 4097], 3, 3), ([5, 1, 2], [700, 2100, 5], 3, 1),
+    ([1500], [1500], 1, 1), ([1500], [1900], 3, 1), ([1500, 1], [1700, 300], 4, 1),
+])
+def test_key_weights_from_zeros(kind, d, qlens, ctx, hq, hkv):
+    """Nothing but what the step adds is there for the bound to be a part of; and runs of 1,500 tokens."""
+    import paged_kv_cache_286_gb300 as pa
+    c = Case(ctx, qlens, hq, hkv, d, kind, seed=sum(ctx) + hq + d)
+    t, cl, qsl = c.dev()
+    before = np.zeros((len(ctx), hkv, max(ctx)), np.float32)
+    W = torch.from_numpy(before).cuda()
+    ws = c.workspace(pa, True)
+    ws[256:] = 0xFF
+    pa.attention_key_weights(c.q.cuda(), c.k, c.v, t, cl, qsl, W, ws, **c.hints())
+    assert pa.check_error(ws) == 0
+    check_weights(c, before, W.cpu().numpy(), list(range(len(ctx))), 1.0)
