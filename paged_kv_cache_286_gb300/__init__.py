@@ -55,7 +55,7 @@ def _stream(stream) -> int:
     """The stream's handle (None: the current device's current stream)."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need(t: torch.Tensor, name: str, dtypes, ndim: int):
@@ -126,12 +126,16 @@ def _on(stream, *tensors):
     """Checks that the tensors (None: absent) share one device and returns a context in which the
     call's allocations and its launch are on that device and on `stream` (None: the device's
     current stream)."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.get_device() != dev:
-            raise ValueError(f"tensors on different devices: {t.device} and {tensors[0].device}")
+    try:
+        dev = tensors[0].get_device()
+        for t in tensors:
+            if t is not None and t.get_device() != dev:
+                raise ValueError(
+                    f"tensors on different devices: {t.device} and {tensors[0].device}")
+    except AttributeError:
+        raise TypeError("the call takes torch.Tensors") from None
     if stream is None:
-        return _HERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+        return _HERE if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)
     if stream.device_index != dev:
         raise ValueError(f"stream of {stream.device} for tensors on {tensors[0].device}")
     return torch.cuda.stream(stream)

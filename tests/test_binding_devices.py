@@ -51,7 +51,7 @@ def log(monkeypatch):
         log.device.pop()
 
     monkeypatch.setattr(pa._lib, "load", lambda: Library(log))
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: log.device[-1])
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: log.device[-1], raising=False)
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(torch.cuda, "stream", lambda s: device(s.device_index))
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 1000 + d, raising=False)
@@ -84,6 +84,13 @@ def test_attention_refuses_pools_of_different_shapes(log, shape):
     with pytest.raises(ValueError, match="shapes differ"):
         mx = dict(k_cache=on((6, 2, 544), torch.uint8), v_cache=on((6, 2, 1088), torch.uint8))
         pa.attention(**step(**mx))
+    assert log == []
+
+
+@pytest.mark.parametrize("name", ["block_tables", "context_lens", "workspace", "out"])
+def test_what_is_no_tensor_is_refused(log, name):
+    with pytest.raises(TypeError):
+        pa.attention(**step(**{name: [[1, 2]]}))
     assert log == []
 
 
