@@ -23,7 +23,8 @@
  *   - Memory: every pointer argument named *_cache, q, k, v, out, slot_mapping, block_tables,
  *     context_lens, query_start_loc, key_weights and workspace is a DEVICE pointer on the current device.
  *     `cache` descriptors are HOST pointers.  The caller allocates and owns all of it; the
- *     library never allocates or frees device memory.
+ *     library never allocates or frees device memory.  A workspace serves one call at a time: calls
+ *     (or captured graphs of them) whose GPU work may overlap need one each.
  *   - Execution: calls are asynchronous on `stream` (0 = legacy default stream) and ordered by
  *     it; nothing synchronises the host except pa_check_error.  pa_cache_append must precede
  *     pa_attention on the same stream when the step's new tokens are to be attended.

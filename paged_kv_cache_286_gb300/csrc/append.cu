@@ -67,8 +67,9 @@ __global__ void __launch_bounds__(256) cache_append_kernel(
   }
 }
 
-// Division of 0 <= n < 2^31 by a fixed d: (n + high word of n * mul) >> shift, with 2^shift the next
-// power of two from d and mul = floor(2^32 (2^shift - d) / d) + 1.  (A 64-bit division by a run-time
+// Division of 0 <= n < 2^31 by a fixed d (Granlund and Montgomery's division by invariant integers):
+// (n + high word of n * mul) >> shift, with 2^shift the next power of two from d and mul = floor(2^32
+// (2^shift - d) / d) + 1.  (A 64-bit division by a run-time
 // value took more instructions than all else that a thread of these kernels does.)
 struct FastDiv {
   uint32_t d, mul, shift;

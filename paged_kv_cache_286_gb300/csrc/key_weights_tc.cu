@@ -13,10 +13,11 @@
 //  * E4M3 and MXFP4 keys become bf16 (exact: four significant bits and two) on their way in, by the
 //    warps 2-17, once per item; copied K tiles cost less, but a conversion beforehand would write
 //    and read four or eight times the bytes.
-//  * A score costs the epilogue an FMA, a 2^x and an add; the 2^x bound it from below (32 a cycle
-//    and SM: 0.5 us a tile of 256 x 128), the MMAs take about as long.  Two runs of 2,048 tokens
-//    x 32 heads after 6,144 (8 kv heads of 128): 338 us for bf16 keys, 712 TFLOP/s, 341 us for E4M3
-//    and 344 us for MXFP4, where the mma.sync kernel took 1,280; one run of 512 x 32 in 2,560 keys
+//  * A score costs the epilogue an FMA, a 2^x and an add: the 2^x (32 a cycle and SM) take 0.5 us of a
+//    tile of 256 x 128, the MMAs 0.7.  A tile takes 1.8: latency bounds it, as a warp reads 32 columns
+//    of an accumulator, waits, and works on them with no read of its own in flight.  Two runs of 2,048
+//    tokens x 32 heads after 6,144 (8 kv heads of 128): 338 us for bf16 keys, 712 TFLOP/s, 341 us for
+//    E4M3 and 344 us for MXFP4, where the mma.sync kernel took 1,280; one run of 512 x 32 in 2,560 keys
 //    beside one of 512 x 32 in 512 31 us.
 //  * Every wait is bounded; when one runs out the CTA records PA_DEVERR_TIMEOUT, stops, lets its
 //    copies and MMAs finish (bounded again) and frees its tensor memory.
